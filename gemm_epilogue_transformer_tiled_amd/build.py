@@ -1,6 +1,7 @@
 """Builds libgemm_epilogue.so (the fused path), libgemm_epilogue_serial.so (its reference build:
-every instance with a mainloop that overlaps nothing, for bit-for-bit race tests) and
-libge_baselines.so (unfused comparators and calibration probes) in-tree with hipcc for gfx950.
+every instance with a mainloop that overlaps nothing, for bit-for-bit race tests),
+libge_block.so (the transformer-block operators around the products) and libge_baselines.so
+(unfused comparators and calibration probes) in-tree with hipcc for gfx950.
 
 Usage: python gemm_epilogue_transformer_tiled_amd/build.py  (runs by path: importing the
 package itself needs the library this script builds)
@@ -19,10 +20,12 @@ ONE_WAVE = [f"ge_tile_{t}_{lay}.hip" for t in ("256x256", "256x128_pair", "128x1
             for lay in ("kn", "nk", "f8")]
 TWO_WAVE = [f"ge_tile_{t}_{lay}.hip" for t in ("256x256w8", "256x128w8_pair") for lay in ("kn", "nk", "f8")]
 COMMON = ["ge_kernels.hip", "noalloc.hip", "tiles.cpp", "api.cpp"]
+BLOCK = ["ge_ffn_pair.hip", "ge_ffn_grad.hip", "ge_ffn_plain.hip", "block_api.cpp"]
 # library -> (its sources, extra compiler flags)
 TARGETS = {
     os.path.join(HERE, "libgemm_epilogue.so"): (ONE_WAVE + TWO_WAVE + COMMON, ()),
     os.path.join(HERE, "libgemm_epilogue_serial.so"): (ONE_WAVE + TWO_WAVE + COMMON, ("-DGE_SERIAL_PIPELINE=1",)),
+    os.path.join(HERE, "libge_block.so"): (BLOCK, ()),
     os.path.join(HERE, "libge_baselines.so"): (["baselines.hip", "probe_mfma16.hip"], ()),
 }
 # per-source compiler flags (the 16x16x32 probe keeps its accumulators in VGPRs: see its header)
