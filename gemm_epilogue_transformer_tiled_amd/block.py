@@ -1,7 +1,8 @@
 """Binding of libge_block.so: the transformer-block operators around the fused products.
 
-The gated feed-forward block with its backward pass (``GatedFFN``).  The functions carry the C
-names of ``include/ge_block.h``; the classes own one handle and its zero-filled workspace, like
+The gated feed-forward block with its backward pass (``GatedFFN``), the per-head norm of queries and
+keys with the position rotation and its gradient (``QKRotary``), the global gradient norm with
+clipping (``GradClip``).  ``lib`` holds the C functions of ``include/ge_block.h``; the classes own one handle and its zero-filled workspace, like
 ``Plan``.  Argument marshalling only: every step of the computation runs in the HIP kernels.
 The classes check shapes, strides, element types and devices of the tensors they are given; the
 library checks pointers and sizes again.
@@ -10,16 +11,20 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+import math
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
-from . import ACT_NAMES, GE_LAYOUT_KN, GE_LAYOUT_NK, GE_OK, GemmEpilogueError
+from . import ACT_NAMES, GE_DT_BF16, GE_DT_FP32, GE_LAYOUT_KN, GE_LAYOUT_NK, GE_OK, GemmEpilogueError
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libge_block.so")
 
 GE_FFN_TILE_256, GE_FFN_TILE_128, GE_FFN_TILE_64, GE_FFN_TILE_COUNT = range(4)
+GE_PAIRS_INTERLEAVED, GE_PAIRS_HALF = range(2)
+PAIR_NAMES = {"interleaved": GE_PAIRS_INTERLEAVED, "half": GE_PAIRS_HALF}
+DTYPES = {torch.bfloat16: GE_DT_BF16, torch.float32: GE_DT_FP32}
 LAYOUT_NAMES = {"kn": GE_LAYOUT_KN, "nk": GE_LAYOUT_NK}
 
 _p, _i32, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -36,6 +41,28 @@ class ge_ffn_args_t(ctypes.Structure):
                                   "workspace")] + [("workspace_bytes", _sz)]
 
 
+class ge_qk_desc_t(ctypes.Structure):
+    _fields_ = [(n, _i64) for n in ("tokens", "heads_q", "heads_k", "q_token", "q_head", "k_token", "k_head",
+                                    "oq_token", "oq_head", "ok_token", "ok_head",
+                                    "dq_token", "dq_head", "dk_token", "dk_head")] + \
+               [(n, _i32) for n in ("head_dim", "rot_dim", "pairs", "norm", "dtype", "pos64")] + [("eps", _f)]
+
+
+class ge_qk_args_t(ctypes.Structure):
+    _fields_ = [(n, _p) for n in ("q", "k", "q_out", "k_out", "positions", "inv_freq", "gain_q", "gain_k",
+                                  "dq_out", "dk_out", "dq", "dk", "dgain_q", "dgain_k", "workspace")] + \
+               [("workspace_bytes", _sz), ("amplitude", _f)]
+
+
+class ge_clip_tensor_t(ctypes.Structure):
+    _fields_ = [("numel", _i64), ("dtype", _i32)]
+
+
+class ge_clip_args_t(ctypes.Structure):
+    _fields_ = [("in_", _p), ("out", _p), ("norm", _p), ("workspace", _p), ("workspace_bytes", _sz),
+                ("max_norm", _f), ("eps", _f)]
+
+
 _SIGS = {
     "ge_ffn_validate": ([ctypes.POINTER(ge_ffn_desc_t)], ctypes.c_int),
     "ge_ffn_create": ([ctypes.POINTER(ge_ffn_desc_t), ctypes.POINTER(_p)], ctypes.c_int),
@@ -44,6 +71,16 @@ _SIGS = {
     "ge_ffn_backward": ([_p, ctypes.POINTER(ge_ffn_args_t), _p], ctypes.c_int),
     "ge_ffn_destroy": ([_p], None),
     "ge_ffn_describe": ([_p, ctypes.c_char_p, _sz], ctypes.c_int),
+    "ge_qk_validate": ([ctypes.POINTER(ge_qk_desc_t)], ctypes.c_int),
+    "ge_qk_create": ([ctypes.POINTER(ge_qk_desc_t), ctypes.POINTER(_p)], ctypes.c_int),
+    "ge_qk_workspace_size": ([_p, ctypes.POINTER(_sz)], ctypes.c_int),
+    "ge_qk_forward": ([_p, ctypes.POINTER(ge_qk_args_t), _p], ctypes.c_int),
+    "ge_qk_backward": ([_p, ctypes.POINTER(ge_qk_args_t), _p], ctypes.c_int),
+    "ge_qk_destroy": ([_p], None),
+    "ge_clip_create": ([ctypes.POINTER(ge_clip_tensor_t), _i32, ctypes.POINTER(_p)], ctypes.c_int),
+    "ge_clip_workspace_size": ([_p, ctypes.POINTER(_sz)], ctypes.c_int),
+    "ge_clip_run": ([_p, ctypes.POINTER(ge_clip_args_t), _p], ctypes.c_int),
+    "ge_clip_destroy": ([_p], None),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -239,3 +276,195 @@ class GatedFFN(_Plan):
 
     def backward(self, args: Args, stream: Optional[int] = None) -> None:
         self._run(args, True, stream)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: int = 4096, slow: float = 1.0, fast: float = 32.0
+                       ) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, amplitude) of the rotation: inv_freq[i] = base^(-2i / rot_dim), fp32 on the host, scaled
+    for contexts ``factor`` times longer than the original.
+
+    none: as they are.  linear: all divided by factor.  base: base * factor^(rot_dim / (rot_dim - 2)), which
+    divides the slowest by factor and leaves the fastest.  by_parts: those that make fewer than ``slow``
+    turns over original_length are divided by factor, those that make more than ``fast`` are kept, those
+    between are blended, and amplitude is 0.1 ln(factor) + 1 (1 for the others)."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim is even and not negative")
+    if not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("factor is at least 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        base = base * factor ** (rot_dim / (rot_dim - 2)) if rot_dim > 2 else base
+    f = base ** (-2.0 * i / max(rot_dim, 1))
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling}")
+    return f.float(), amplitude
+
+
+def make_qk_args(q=None, k=None, q_out=None, k_out=None, positions=None, inv_freq=None, amplitude: float = 1.0,
+                 gain_q=None, gain_k=None, dq_out=None, dk_out=None, dq=None, dk=None, dgain_q=None, dgain_k=None,
+                 workspace=None) -> Args:
+    """Pointer pack of the query/key norm with rotation: tensors [tokens][heads][head_dim] (any strides
+    over tokens and heads), gains [head_dim], positions [tokens], inv_freq [rot_dim / 2]."""
+    a = Args(ge_qk_args_t(), dict(q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=inv_freq,
+                                  gain_q=gain_q, gain_k=gain_k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk,
+                                  dgain_q=dgain_q, dgain_k=dgain_k, workspace=workspace))
+    a.c.amplitude = amplitude
+    a.c.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return a
+
+
+class QKRotary(_Plan):
+    """Per-head RMS norm of queries and keys with the position rotation, and its gradient.
+
+    ``forward`` reads q, k, positions, inv_freq (and the gains), writes q_out, k_out (which may be q and
+    k); ``backward`` reads dq_out, dk_out (and, with the norm, q, k and the gains), writes dq, dk and, with
+    the norm, dgain_q, dgain_k.  ``*_strides``: (token, head) strides in elements, default packed; the
+    gradients of the outputs have the outputs' strides, dq and dk those of q and k unless given."""
+
+    _destroy = "ge_qk_destroy"
+
+    def __init__(self, tokens: int, heads_q: int, heads_k: int, head_dim: int, rot_dim: Optional[int] = None,
+                 pairs: str = "half", norm: bool = True, eps: float = 1e-6, dtype=torch.bfloat16,
+                 q_strides: Optional[Sequence[int]] = None, k_strides: Optional[Sequence[int]] = None,
+                 q_out_strides: Optional[Sequence[int]] = None, k_out_strides: Optional[Sequence[int]] = None,
+                 dq_strides: Optional[Sequence[int]] = None, dk_strides: Optional[Sequence[int]] = None,
+                 positions_dtype=torch.int64, device="cuda"):
+        super().__init__(device)
+        if dtype not in DTYPES:
+            raise ValueError(f"element type {dtype}: bfloat16 or float32")
+        if positions_dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"positions of type {positions_dtype}: int32 or int64")
+        self.dtype, self.positions_dtype = dtype, positions_dtype
+        q = tuple(q_strides or (heads_q * head_dim, head_dim))
+        k = tuple(k_strides or (heads_k * head_dim, head_dim))
+        oq = tuple(q_out_strides or (heads_q * head_dim, head_dim))
+        ok = tuple(k_out_strides or (heads_k * head_dim, head_dim))
+        dq, dk = tuple(dq_strides or q), tuple(dk_strides or k)
+        self.strides = dict(q=q, k=k, q_out=oq, k_out=ok, dq_out=oq, dk_out=ok, dq=dq, dk=dk)
+        self.desc = ge_qk_desc_t(tokens, heads_q, heads_k, *q, *k, *oq, *ok, *dq, *dk, head_dim,
+                                 head_dim if rot_dim is None else rot_dim, PAIR_NAMES[pairs], int(norm), DTYPES[dtype],
+                                 int(positions_dtype == torch.int64), eps)
+        out = _p()
+        _check(lib.ge_qk_create(ctypes.byref(self.desc), ctypes.byref(out)), "ge_qk_create")
+        self.handle = out.value
+        n = _sz()
+        _check(lib.ge_qk_workspace_size(self.handle, ctypes.byref(n)), "ge_qk_workspace_size")
+        self.workspace_bytes = n.value
+        self.workspace = None        # made by the first backward
+
+    def _fit(self, args: Args, backward: bool) -> None:
+        c = self.desc
+        T, D = c.tokens, c.head_dim
+        names = (("q", "k") if c.norm else ()) + ("dq_out", "dk_out", "dq", "dk") if backward else ("q", "k", "q_out", "k_out")
+        for n in names:
+            heads = c.heads_q if "q" in n else c.heads_k
+            self._tensor(args, n, (T, heads, D), self.dtype, (*self.strides[n], 1))
+        if c.rot_dim and T:
+            self._tensor(args, "positions", (T,), self.positions_dtype, (1,))
+            self._tensor(args, "inv_freq", (c.rot_dim // 2,), torch.float32, (1,))
+        if c.norm:
+            for s, heads in (("q", c.heads_q), ("k", c.heads_k)):
+                if heads:
+                    self._tensor(args, "gain_" + s, (D,), self.dtype, (1,))
+                    if backward:
+                        self._tensor(args, "dgain_" + s, (D,), torch.float32, (1,))
+            if backward and args.tensors["workspace"] is None and self.workspace is None:
+                self.workspace = self._scratch(self.workspace_bytes)
+
+    def _run(self, args: Args, backward: bool, stream: Optional[int]) -> None:
+        fits = args._fits.get(self, ())
+        if backward not in fits:
+            self._fit(args, backward)
+            args._fits[self] = (*fits, backward)
+        if backward and self.workspace is not None and args.tensors["workspace"] is None:
+            args.c.workspace, args.c.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
+        call = lib.ge_qk_backward if backward else lib.ge_qk_forward
+        st = call(self.handle, args._ref, self._stream(stream))
+        if st != GE_OK:
+            raise GemmEpilogueError(st, "ge_qk_backward" if backward else "ge_qk_forward")
+
+    def forward(self, args: Args, stream: Optional[int] = None) -> None:
+        self._run(args, False, stream)
+
+    def backward(self, args: Args, stream: Optional[int] = None) -> None:
+        self._run(args, True, stream)
+
+
+def make_clip_args(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None, norm=None,
+                   max_norm: float = 1.0, eps: float = 1e-6, workspace=None) -> Args:
+    """Pointer pack of the clipping: the gradients, the tensors their clipped values go to (the gradients
+    themselves to clip in place; None: only the norm) and a float32 tensor of one element for the norm."""
+    grads = list(grads)
+    outs = None if outs is None else list(outs)
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError("as many outputs as gradients")
+    a = Args(ge_clip_args_t(), dict(norm=norm, workspace=workspace))
+    a.grads, a.outs = grads, outs
+    a._in = (_p * max(len(grads), 1))(*[g.data_ptr() for g in grads])
+    a.c.in_ = ctypes.cast(a._in, _p)
+    if outs is not None:
+        a._out = (_p * max(len(outs), 1))(*[g.data_ptr() for g in outs])
+        a.c.out = ctypes.cast(a._out, _p)
+    a.c.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    a.c.max_norm, a.c.eps = max_norm, eps
+    return a
+
+
+class GradClip(_Plan):
+    """The global norm of a list of gradients (bf16 and fp32 mixed, each dense) and their clipping:
+    every gradient times min(1, max_norm / (norm + eps)).  Made for a list of tensors of given sizes and
+    types; ``run`` takes any pack of tensors like them."""
+
+    _destroy = "ge_clip_destroy"
+
+    def __init__(self, grads: Sequence[torch.Tensor], device=None):
+        grads = list(grads)
+        super().__init__(device if device is not None else grads[0].device if grads else "cuda")
+        for g in grads:
+            if g.dtype not in DTYPES:
+                raise ValueError(f"gradient of type {g.dtype}: bfloat16 or float32")
+        self.like = [(g.numel(), g.dtype) for g in grads]
+        table = (ge_clip_tensor_t * max(len(grads), 1))(*[(n, DTYPES[t]) for n, t in self.like])
+        out = _p()
+        _check(lib.ge_clip_create(table, len(grads), ctypes.byref(out)), "ge_clip_create")
+        self.handle = out.value
+        n = _sz()
+        _check(lib.ge_clip_workspace_size(self.handle, ctypes.byref(n)), "ge_clip_workspace_size")
+        self.workspace = self._scratch(n.value)
+
+    def _fit(self, args: Args) -> None:
+        if args.outs is None and args.tensors["norm"] is None:
+            raise ValueError("neither a norm nor outputs to write")
+        if args.tensors["norm"] is not None:
+            self._tensor(args, "norm", (1,), torch.float32)
+        for kind in (args.grads, args.outs):
+            if kind is None:
+                continue
+            if len(kind) != len(self.like):
+                raise ValueError(f"{len(kind)} tensors, the plan has {len(self.like)}")
+            for i, (g, like) in enumerate(zip(kind, self.like)):
+                if (g.numel(), g.dtype) != like:
+                    raise ValueError(f"tensor {i} has {g.numel()} values of {g.dtype}, the plan {like}")
+                if g.device != self.device:
+                    raise ValueError(f"tensor {i} is on {g.device}, the plan on {self.device}")
+                if not g.is_contiguous():
+                    raise ValueError(f"tensor {i} is not contiguous")
+
+    def run(self, args: Args, stream: Optional[int] = None) -> None:
+        if self not in args._fits:
+            self._fit(args)
+            args._fits[self] = True
+        if args.tensors["workspace"] is None:
+            args.c.workspace, args.c.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
+        st = lib.ge_clip_run(self.handle, args._ref, self._stream(stream))
+        if st != GE_OK:
+            raise GemmEpilogueError(st, "ge_clip_run")

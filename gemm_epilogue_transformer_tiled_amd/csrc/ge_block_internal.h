@@ -42,4 +42,49 @@ hipError_t launch_ffn_pair(int tile, int act, bool b_nk, const FfnLaunch& l, hip
 hipError_t launch_ffn_grad(int tile, int act, bool b_nk, const FfnLaunch& l, hipStream_t s);
 hipError_t launch_ffn_plain(int mode, int tile, bool b_nk, const FfnLaunch& l, hipStream_t s);
 
+// ---- query/key norm with rotation ----
+struct QkParams {
+  const void* x[2];           // q, k (forward, and backward with norm)
+  void* y[2];                 // forward: outputs; backward: gradients of the inputs
+  const void* dy[2];          // backward: gradients of the outputs
+  const void* gain[2];
+  const void* positions;
+  const float* inv_freq;
+  float* part;                // backward with norm: partial gain gradients [workgroups][2][head_dim]
+  int64_t xt[2], xh[2], yt[2], yh[2], dt[2], dh[2];   // token and head strides of x, y, dy
+  int64_t tokens;
+  int32_t heads[2];
+  int32_t head_dim, rot_dim;
+  int32_t group;              // lanes per head: a power of two, 8 values a lane
+  int32_t tokens_per_wg;      // tokens of one turn of a workgroup
+  int32_t head_splits;        // workgroups that share a token's heads
+  int32_t workgroups;         // grid.x
+  bool pos64;
+  float eps, amplitude;
+};
+struct QkKind { bool bf16, wide, half, norm, backward; };
+hipError_t launch_qk(const QkKind& kind, const QkParams& p, hipStream_t s);
+hipError_t launch_qk_gains(const float* part, int rows, int head_dim, float* dgain_q, float* dgain_k, hipStream_t s);
+constexpr int kQkThreads = 256;
+constexpr int kQkMaxAngles = 1024;      // angles of one turn kept in LDS (8 KB)
+constexpr int kQkMaxBackwardGrid = 768;
+
+// ---- gradient norm and clipping ----
+constexpr int kClipTensors = 128;       // tensors of one launch (its table travels as the argument)
+constexpr int kClipPartials = 2048;     // workgroups of all norm launches of a call together
+constexpr int kClipChunk = 16384;       // values of one workgroup's turn
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t numel[kClipTensors];
+  uint32_t chunk0[kClipTensors + 1];    // first chunk of each tensor; [n]: all chunks
+  uint32_t fp32[kClipTensors / 32];     // bit t: tensor t is fp32
+  int32_t n;
+};
+hipError_t launch_clip_norm(const ClipTable& t, int grid, double* part, hipStream_t s);
+// nparts partial sums -> *norm (if any)
+hipError_t launch_clip_finish(const double* part, int nparts, float* norm, hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable& t, int grid, const double* part, int nparts, float max_norm, float eps,
+                             float* norm, hipStream_t s);
+
 }  // namespace ge

@@ -137,29 +137,29 @@ void ffn_product(FfnLaunch l) {
   auto kpos = [&](int j) { return (second(j) ? j - seg : j) * 32; };
   __amdgpu_buffer_rsrc_t ars, brs, brs2;
   int a_lim = 0, b_lim = 0;                            // row operands: K values left from the step's first
+  // (32-bit byte extents: leading dimensions are below 2^22 elements, checked on the host)
+  const uint16_t* const pa = p.A + a_at;
+  const uint16_t* const pa2 = DUAL ? p.A2 + a_at : pa;
+  const uint16_t* const pb = p.B + b_at;
+  const uint16_t* const pb2 = (DUAL || PAIR) ? p.B2 + b_at : pb;
+  auto extent = [](bool col, int lim, int rows, uint32_t ld2) -> int {
+    const int whole = col ? (min(lim, 64) - 1) * (int)ld2 + rows * 2 : (rows - 1) * (int)ld2 + lim * 2;
+    return lim > 0 ? whole : 0;
+  };
+  auto at_k = [](bool col, const uint16_t* base, int k0, uint32_t ld2) -> const void* {
+    return (const unsigned char*)base + (col ? (uint64_t)(uint32_t)k0 * ld2 : (uint64_t)((uint32_t)k0 * 2u));
+  };
   auto set_a = [&](int j) {
-    const uint16_t* base = (second(j) ? p.A2 : p.A) + a_at;
     const int k0 = kpos(j);
     a_lim = K - k0;
-    if constexpr (AC)
-      ars = make_rsrc(base + (int64_t)k0 * p.lda, a_lim > 0 ? (int64_t)(uint32_t)(min(a_lim, 64) - 1) * lda2 + mrows * 2 : 0);
-    else
-      ars = make_rsrc(base + k0, a_lim > 0 ? (int64_t)(uint32_t)(mrows - 1) * lda2 + a_lim * 2 : 0);
+    ars = make_rsrc(at_k(AC, second(j) ? pa2 : pa, k0, lda2), extent(AC, a_lim, mrows, lda2));
   };
   auto set_b = [&](int j) {
-    const uint16_t* base = (second(j) ? p.B2 : p.B) + b_at;
     const int k0 = kpos(j);
     b_lim = K - k0;
-    int64_t ext;
-    if constexpr (BC) {
-      ext = b_lim > 0 ? (int64_t)(uint32_t)(min(b_lim, 64) - 1) * ldb2 + ncols * 2 : 0;
-      brs = make_rsrc(base + (int64_t)k0 * p.ldb, ext);
-      if constexpr (PAIR) brs2 = make_rsrc(p.B2 + b_at + (int64_t)k0 * p.ldb, ext);
-    } else {
-      ext = b_lim > 0 ? (int64_t)(uint32_t)(ncols - 1) * ldb2 + b_lim * 2 : 0;
-      brs = make_rsrc(base + k0, ext);
-      if constexpr (PAIR) brs2 = make_rsrc(p.B2 + b_at + k0, ext);
-    }
+    const int ext = extent(BC, b_lim, ncols, ldb2);
+    brs = make_rsrc(at_k(BC, second(j) ? pb2 : pb, k0, ldb2), ext);
+    if constexpr (PAIR) brs2 = make_rsrc(at_k(BC, pb2, k0, ldb2), ext);
   };
 
   // ---- direct loads: per-lane offsets, fixed for the whole loop ----
@@ -192,22 +192,31 @@ void ffn_product(FfnLaunch l) {
       b_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * ldb2 + (r_x ^ (u & 3u)) * 16u;
     }
   }
+  // Row operands: chunks past K get the out-of-range offset.  The chunk index is recomputed per
+  // fill (its input is opaque): kept in registers across the loop it spills the 256-row tiles.
+  auto chunk_base = [&]() {
+    uint32_t x = r_x;
+    asm volatile("" : "+v"(x));
+    return x;
+  };
   auto issue_a = [&](unsigned char* slot) {
+    const uint32_t x = AC ? 0u : chunk_base();
 #pragma unroll
     for (int t = 0; t < T::LA; ++t) {
       const uint32_t u = (uint32_t)(wave * T::LA + t);
       uint32_t off = a_voff[t];
-      if constexpr (!AC) off = (int)((r_x ^ (u & 3u)) * 8u) < a_lim ? off : kOOB;
+      if constexpr (!AC) off = (int)((x ^ (u & 3u)) * 8u) < a_lim ? off : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (__attribute__((address_space(3))) void*)(slot + u * 1024), 16, off,
                                                0, 0, 0);
     }
   };
   auto issue_b = [&](unsigned char* dst) {
+    const uint32_t x = BC ? 0u : chunk_base();
 #pragma unroll
     for (int t = 0; t < LBF; ++t) {
       const uint32_t g = (uint32_t)(wave * LBF + t), u = g % (uint32_t)B_UNITS;   // wave-uniform
       uint32_t off = b_voff[t];
-      if constexpr (!BC) off = (int)((r_x ^ (u & 3u)) * 8u) < b_lim ? off : kOOB;
+      if constexpr (!BC) off = (int)((x ^ (u & 3u)) * 8u) < b_lim ? off : kOOB;
       if (PAIR && g >= (uint32_t)B_UNITS)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(brs2, (__attribute__((address_space(3))) void*)(dst + g * 1024), 16, off,
                                                  0, 0, 0);

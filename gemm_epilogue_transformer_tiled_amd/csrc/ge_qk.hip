@@ -1,0 +1,332 @@
+// Per-head norm of queries and keys with the position rotation, forward and backward (gfx950).
+//
+// Memory-bound: every value is read once and written once (backward: the gradient and, with the
+// norm, the input are read).  A head lies on a group of lanes, eight values a lane, chosen so
+// that both values of every rotation pair are in one lane: interleaved pairs are eight
+// consecutive values, half pairs four consecutive values of each half.  So the rotation needs no
+// exchange between lanes, a lane reads and writes the same elements (in place is safe), and only
+// the norm's sums cross lanes.
+//
+// The angle position * inv_freq and its reduction to a turn are computed in 64 bits (positions go
+// past 2^24 turns' worth of fp32), its cosine and sine in 32, once per token and pair: a
+// workgroup computes those of its tokens into LDS and all heads of the tokens read them there.
+#include "ge_block_internal.h"
+
+namespace ge {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const bf16x2 h = {(__bf16)a, (__bf16)b};      // round to nearest even
+  return __builtin_bit_cast(uint32_t, h);
+}
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float one(const float* p) { return *p; }
+__device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)(pack2(v, 0.0f) & 0xFFFFu); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+
+// The eight values of a lane: pair j is (a[j], b[j]).
+struct Pairs {
+  float a[4], b[4];
+};
+
+// Element offsets of pair j of a lane's slots slot .. slot + 3, of the head's head_dim / 2 pairs; the
+// first rot_dim / 2 of them are turned.  The pairing of the others does not matter: half pairs take
+// the lane's eight values as two runs of four where whole lanes are unturned (the same in the wide
+// and the general kernels, so that both add up a head in the same order), and otherwise neighbours.
+template <bool HALF>
+__device__ __forceinline__ int offset_a(int slot, int j, int rot2, int d2) {
+  if (HALF && slot + j < rot2) return slot + j;
+  if (HALF && ((rot2 | d2) & 3) == 0) return 2 * slot + j;
+  return 2 * (slot + j);
+}
+template <bool HALF>
+__device__ __forceinline__ int offset_b(int slot, int j, int rot2, int d2) {
+  if (HALF && slot + j < rot2) return slot + j + rot2;
+  if (HALF && ((rot2 | d2) & 3) == 0) return 2 * slot + 4 + j;
+  return 2 * (slot + j) + 1;
+}
+
+// WIDE: rot_dim / 2 and head_dim / 2 multiples of four and 16-byte aligned heads, so a lane's slots are
+// all turned or all not, and its values are two runs of four (or one of eight).
+template <class E, bool WIDE, bool HALF>
+__device__ __forceinline__ Pairs load(const E* head, int slot, int rot2, int d2) {
+  Pairs v;
+  if constexpr (WIDE) {
+    if constexpr (HALF) {
+      // not turned: the pairing does not matter, take the runs as they come
+      const int oa = slot < rot2 ? slot : 2 * slot, ob = slot < rot2 ? slot + rot2 : 2 * slot + 4;
+      if constexpr (sizeof(E) == 2) {
+        const u32x2 x = *(const u32x2*)(head + oa), y = *(const u32x2*)(head + ob);
+        v.a[0] = lo(x[0]); v.a[1] = hi(x[0]); v.a[2] = lo(x[1]); v.a[3] = hi(x[1]);
+        v.b[0] = lo(y[0]); v.b[1] = hi(y[0]); v.b[2] = lo(y[1]); v.b[3] = hi(y[1]);
+      } else {
+        const f32x4 x = *(const f32x4*)(head + oa), y = *(const f32x4*)(head + ob);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { v.a[j] = x[j]; v.b[j] = y[j]; }
+      }
+    } else if constexpr (sizeof(E) == 2) {
+      const u32x4 x = *(const u32x4*)(head + 2 * slot);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { v.a[j] = lo(x[j]); v.b[j] = hi(x[j]); }
+    } else {
+      const f32x4 x = *(const f32x4*)(head + 2 * slot), y = *(const f32x4*)(head + 2 * slot + 4);
+      v.a[0] = x[0]; v.b[0] = x[1]; v.a[1] = x[2]; v.b[1] = x[3];
+      v.a[2] = y[0]; v.b[2] = y[1]; v.a[3] = y[2]; v.b[3] = y[3];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool ok = slot + j < d2;
+      v.a[j] = ok ? one(head + offset_a<HALF>(slot, j, rot2, d2)) : 0.0f;
+      v.b[j] = ok ? one(head + offset_b<HALF>(slot, j, rot2, d2)) : 0.0f;
+    }
+  }
+  return v;
+}
+
+template <class E, bool WIDE, bool HALF>
+__device__ __forceinline__ void store(E* head, int slot, int rot2, int d2, const Pairs& v) {
+  if constexpr (WIDE) {
+    if constexpr (HALF) {
+      const int oa = slot < rot2 ? slot : 2 * slot, ob = slot < rot2 ? slot + rot2 : 2 * slot + 4;
+      if constexpr (sizeof(E) == 2) {
+        *(u32x2*)(head + oa) = u32x2{pack2(v.a[0], v.a[1]), pack2(v.a[2], v.a[3])};
+        *(u32x2*)(head + ob) = u32x2{pack2(v.b[0], v.b[1]), pack2(v.b[2], v.b[3])};
+      } else {
+        *(f32x4*)(head + oa) = f32x4{v.a[0], v.a[1], v.a[2], v.a[3]};
+        *(f32x4*)(head + ob) = f32x4{v.b[0], v.b[1], v.b[2], v.b[3]};
+      }
+    } else if constexpr (sizeof(E) == 2) {
+      *(u32x4*)(head + 2 * slot) = u32x4{pack2(v.a[0], v.b[0]), pack2(v.a[1], v.b[1]), pack2(v.a[2], v.b[2]),
+                                         pack2(v.a[3], v.b[3])};
+    } else {
+      *(f32x4*)(head + 2 * slot) = f32x4{v.a[0], v.b[0], v.a[1], v.b[1]};
+      *(f32x4*)(head + 2 * slot + 4) = f32x4{v.a[2], v.b[2], v.a[3], v.b[3]};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (slot + j < d2) {
+        put(head + offset_a<HALF>(slot, j, rot2, d2), v.a[j]);
+        put(head + offset_b<HALF>(slot, j, rot2, d2), v.b[j]);
+      }
+  }
+}
+
+template <class E, bool WIDE, bool HALF, bool NORM, bool BWD>
+__global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
+  __shared__ float2 turn[kQkMaxAngles];
+  __shared__ float gsum[BWD && NORM ? 2 * 8 * kQkThreads : 1];
+  const int tid = threadIdx.x, G = p.group;
+  const int gl = tid & (G - 1), ng = kQkThreads / G, grp = tid / G;
+  const int slot = 4 * gl, rot2 = p.rot_dim / 2, d2 = p.head_dim / 2;
+  const bool live = slot < d2;
+  const int heads = p.heads[0] + p.heads[1];
+  const float inv_d = 1.0f / (float)p.head_dim;
+
+  Pairs gain[2];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool ok = p.heads[w] > 0 && slot + j < d2;
+        gain[w].a[j] = ok ? one((const E*)p.gain[w] + offset_a<HALF>(slot, j, rot2, d2)) : 0.0f;
+        gain[w].b[j] = ok ? one((const E*)p.gain[w] + offset_b<HALF>(slot, j, rot2, d2)) : 0.0f;
+      }
+  }
+  Pairs dgain[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dgain[w].a[j] = dgain[w].b[j] = 0.0f;
+
+  const int tw = p.tokens_per_wg, hs = p.head_splits;
+  const int64_t turns = (p.tokens + tw - 1) / tw * hs;
+  for (int64_t it = blockIdx.x; it < turns; it += gridDim.x) {
+    const int64_t t0 = it / hs * tw;
+    const int part = (int)(it % hs);
+    const int nt = (int)(p.tokens - t0 < tw ? p.tokens - t0 : tw);
+    if (rot2 > 0) {
+      __syncthreads();                                 // the last turn's readers are done
+      for (int i = tid; i < nt * rot2; i += kQkThreads) {
+        const int t = i / rot2, f = i - t * rot2;
+        const double pos = p.pos64 ? (double)((const int64_t*)p.positions)[t0 + t] : (double)((const int32_t*)p.positions)[t0 + t];
+        double turns_of = pos * (double)p.inv_freq[f] * 0.15915494309189533577;     // angle / 2 pi
+        turns_of -= __builtin_rint(turns_of);
+        float s, c;
+        sincospif(2.0f * (float)turns_of, &s, &c);
+        turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+      }
+      __syncthreads();
+    }
+    // (token, head) items of this turn, one per group and step; a split takes every hs-th run of heads
+    const int h_lo = (int)((int64_t)heads * part / hs), nh = (int)((int64_t)heads * (part + 1) / hs) - h_lo;
+    if (nh <= 0) continue;                             // uniform
+    const int step_t = ng / nh, step_h = ng - step_t * nh;
+    int t = grp / nh, h = grp - t * nh;
+    while (t < nt) {
+      const int hh = h_lo + h, w = hh >= p.heads[0] ? 1 : 0, hw = hh - (w ? p.heads[0] : 0);
+      const int64_t tok = t0 + t;
+      Pairs x, d, o;
+      if constexpr (!BWD || NORM) {
+        const E* px = (const E*)p.x[w] + tok * p.xt[w] + hw * p.xh[w];
+        if (live) x = load<E, WIDE, HALF>(px, slot, rot2, d2);
+      }
+      if constexpr (BWD) {
+        const E* pd = (const E*)p.dy[w] + tok * p.dt[w] + hw * p.dh[w];
+        if (live) d = load<E, WIDE, HALF>(pd, slot, rot2, d2);
+      }
+      float cs[4], sn[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cs[j] = 1.0f;
+        sn[j] = 0.0f;
+        if (slot + j < rot2) {
+          const float2 a = turn[t * rot2 + slot + j];
+          cs[j] = a.x;
+          sn[j] = a.y;
+        }
+      }
+      if (!live) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.a[j] = x.b[j] = d.a[j] = d.b[j] = 0.0f;
+      }
+      if constexpr (!BWD) {
+        if constexpr (NORM) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ss += x.a[j] * x.a[j] + x.b[j] * x.b[j];
+          for (int m = 1; m < G; m <<= 1) ss += __shfl_xor(ss, m);
+          const float r = 1.0f / sqrtf(ss * inv_d + p.eps);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x.a[j] = x.a[j] * r * (w ? gain[1].a[j] : gain[0].a[j]);
+            x.b[j] = x.b[j] * r * (w ? gain[1].b[j] : gain[0].b[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o.a[j] = x.a[j] * cs[j] - x.b[j] * sn[j];
+          o.b[j] = x.b[j] * cs[j] + x.a[j] * sn[j];
+        }
+      } else {
+        // the rotation's transpose, then the norm's derivative: with n = x r and e = dy * gain,
+        // dx = r (e - n mean(e n)) and dgain += dy n
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o.a[j] = d.a[j] * cs[j] + d.b[j] * sn[j];
+          o.b[j] = d.b[j] * cs[j] - d.a[j] * sn[j];
+        }
+        if constexpr (NORM) {
+          float ss = 0.0f, ex = 0.0f;
+          Pairs e;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e.a[j] = o.a[j] * (w ? gain[1].a[j] : gain[0].a[j]);
+            e.b[j] = o.b[j] * (w ? gain[1].b[j] : gain[0].b[j]);
+            ss += x.a[j] * x.a[j] + x.b[j] * x.b[j];
+            ex += e.a[j] * x.a[j] + e.b[j] * x.b[j];
+          }
+          for (int m = 1; m < G; m <<= 1) {
+            ss += __shfl_xor(ss, m);
+            ex += __shfl_xor(ex, m);
+          }
+          const float r = 1.0f / sqrtf(ss * inv_d + p.eps);
+          const float mean = ex * r * inv_d;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float na = x.a[j] * r, nb = x.b[j] * r;
+            const float ga = o.a[j] * na, gb = o.b[j] * nb;
+            dgain[0].a[j] += w ? 0.0f : ga;
+            dgain[0].b[j] += w ? 0.0f : gb;
+            dgain[1].a[j] += w ? ga : 0.0f;
+            dgain[1].b[j] += w ? gb : 0.0f;
+            o.a[j] = r * (e.a[j] - na * mean);
+            o.b[j] = r * (e.b[j] - nb * mean);
+          }
+        }
+      }
+      if (live) store<E, WIDE, HALF>((E*)p.y[w] + tok * p.yt[w] + hw * p.yh[w], slot, rot2, d2, o);
+      t += step_t;
+      h += step_h;
+      if (h >= nh) {
+        h -= nh;
+        ++t;
+      }
+    }
+  }
+
+  if constexpr (BWD && NORM) {
+    // the groups' sums meet in LDS and are added in group order
+    const int D = p.head_dim;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (slot + j < d2) {
+          gsum[(grp * 2 + w) * D + offset_a<HALF>(slot, j, rot2, d2)] = dgain[w].a[j];
+          gsum[(grp * 2 + w) * D + offset_b<HALF>(slot, j, rot2, d2)] = dgain[w].b[j];
+        }
+    __syncthreads();
+    for (int i = tid; i < 2 * D; i += kQkThreads) {
+      float s = 0.0f;
+      for (int g = 0; g < ng; ++g) s += gsum[g * 2 * D + i];
+      p.part[(int64_t)blockIdx.x * 2 * D + i] = s;
+    }
+  }
+}
+
+// Sums the workgroups' partial gain gradients, 16 columns a workgroup, 16 threads a column, in a
+// fixed order and in 64 bits.
+__global__ __launch_bounds__(256) void qk_gains(const float* part, int rows, int head_dim, float* dq, float* dk) {
+  __shared__ double sums[16][17];
+  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+  double s = 0.0;
+  if (col < 2 * head_dim)
+    for (int r = r0; r < rows; r += 16) s += (double)part[(int64_t)r * 2 * head_dim + col];
+  sums[r0][c] = s;
+  __syncthreads();
+  if (r0 == 0 && col < 2 * head_dim) {
+    double all = 0.0;
+    for (int r = 0; r < 16; ++r) all += sums[r][c];
+    float* out = col < head_dim ? dq : dk;
+    if (out) out[col < head_dim ? col : col - head_dim] = (float)all;
+  }
+}
+
+template <class E, bool WIDE, bool HALF>
+hipError_t go(const QkKind& k, const QkParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.workgroups), block(kQkThreads);
+  if (k.backward && k.norm) hipLaunchKernelGGL((qk_rotary<E, WIDE, HALF, true, true>), grid, block, 0, s, p);
+  else if (k.backward) hipLaunchKernelGGL((qk_rotary<E, WIDE, HALF, false, true>), grid, block, 0, s, p);
+  else if (k.norm) hipLaunchKernelGGL((qk_rotary<E, WIDE, HALF, true, false>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((qk_rotary<E, WIDE, HALF, false, false>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+template <class E>
+hipError_t go(const QkKind& k, const QkParams& p, hipStream_t s) {
+  if (k.wide) return k.half ? go<E, true, true>(k, p, s) : go<E, true, false>(k, p, s);
+  return k.half ? go<E, false, true>(k, p, s) : go<E, false, false>(k, p, s);
+}
+
+}  // namespace
+
+hipError_t launch_qk(const QkKind& k, const QkParams& p, hipStream_t s) {
+  if (p.workgroups <= 0) return hipSuccess;
+  return k.bf16 ? go<uint16_t>(k, p, s) : go<float>(k, p, s);
+}
+
+hipError_t launch_qk_gains(const float* part, int rows, int head_dim, float* dq, float* dk, hipStream_t s) {
+  hipLaunchKernelGGL(qk_gains, dim3((unsigned)((2 * head_dim + 15) / 16)), dim3(256), 0, s, part, rows, head_dim, dq, dk);
+  return hipGetLastError();
+}
+
+}  // namespace ge

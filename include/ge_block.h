@@ -104,6 +104,108 @@ void ge_ffn_destroy(ge_ffn_handle_t handle);
 /* One line on the kernels the handle launches. */
 ge_status_t ge_ffn_describe(ge_ffn_handle_t handle, char* buf, size_t len);
 
+/* ---------------------------------------------------------------------------------------------
+ * Per-head norm of queries and keys with the position rotation, in one pass.  For each token and
+ * head with D = head_dim values x (fp32 arithmetic, one rounding at the end):
+ *
+ *   r = 1 / sqrt(mean(x^2) + eps)    y = x * r * gain         (desc.norm; otherwise y = x)
+ *   angle_i = position * inv_freq[i], i < rot_dim / 2          (product and reduction in 64 bits)
+ *   (y_a, y_b) -> amplitude * (y_a cos - y_b sin, y_b cos + y_a sin)    for each pair i
+ *   GE_PAIRS_HALF:        a = i, b = i + rot_dim / 2
+ *   GE_PAIRS_INTERLEAVED: a = 2i, b = 2i + 1
+ *   values rot_dim .. D-1 are y, unturned
+ *
+ * Scaled positions for long contexts are a choice of inv_freq and amplitude, which the caller
+ * gives.  Backward: from the gradients of the outputs, those of x (the inputs are read again and
+ * the norm is rebuilt) and of the two gains (fp32 sums over tokens and heads in a fixed order).
+ *
+ * Element types: q, k, their outputs and gradients and the gains all bf16 or all fp32; inv_freq
+ * fp32 [rot_dim / 2]; positions int32 or int64 [tokens], |position| < 2^31; gains' gradients
+ * fp32 [D].  Any of tokens, heads_q, heads_k may be 0.  head_dim even, 2 .. 512; rot_dim even,
+ * 0 .. head_dim (0: only the norm).  Value e of head j of token t is at t * *_token + j * *_head
+ * + e; strides are non-negative, and those of outputs keep elements apart.  Outputs may be the
+ * inputs themselves (same pointer and strides), otherwise they must not overlap inputs or each
+ * other.  Pointers need their element's alignment; 16-byte aligned pointers and strides that are
+ * multiples of 8 elements, with head_dim and rot_dim multiples of 8, take wide accesses.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { GE_PAIRS_INTERLEAVED = 0, GE_PAIRS_HALF = 1 } ge_pairs_t;
+
+typedef struct {
+  int64_t tokens, heads_q, heads_k;
+  int64_t q_token, q_head, k_token, k_head;         /* inputs q, k */
+  int64_t oq_token, oq_head, ok_token, ok_head;     /* outputs; backward: their gradients */
+  int64_t dq_token, dq_head, dk_token, dk_head;     /* backward: gradients of the inputs */
+  int32_t head_dim, rot_dim;
+  int32_t pairs;                                    /* ge_pairs_t */
+  int32_t norm;                                     /* 1: normalise, with gains */
+  int32_t dtype;                                    /* GE_DT_BF16 or GE_DT_FP32 */
+  int32_t pos64;                                    /* 1: positions are int64, 0: int32 */
+  float eps;                                        /* finite, >= 0 */
+} ge_qk_desc_t;
+
+typedef struct {
+  const void *q, *k;                  /* forward; backward with norm */
+  void *q_out, *k_out;                /* forward */
+  const void* positions;              /* with rot_dim > 0 */
+  const float* inv_freq;              /* with rot_dim > 0 */
+  const void *gain_q, *gain_k;        /* with norm */
+  const void *dq_out, *dk_out;        /* backward */
+  void *dq, *dk;                      /* backward */
+  float *dgain_q, *dgain_k;           /* backward with norm: overwritten */
+  void* workspace;                    /* backward with norm */
+  size_t workspace_bytes;
+  float amplitude;
+} ge_qk_args_t;
+
+typedef struct ge_qk_plan* ge_qk_handle_t;
+
+ge_status_t ge_qk_validate(const ge_qk_desc_t* desc);
+ge_status_t ge_qk_create(const ge_qk_desc_t* desc, ge_qk_handle_t* out);
+/* Workspace bytes of ge_qk_backward (partial sums of the gains' gradients; it needs no zero fill);
+ * 0 without norm.  ge_qk_forward needs none. */
+ge_status_t ge_qk_workspace_size(ge_qk_handle_t handle, size_t* bytes);
+/* One launch. */
+ge_status_t ge_qk_forward(ge_qk_handle_t handle, const ge_qk_args_t* args, void* stream);
+/* One launch, and with norm a second one for the gains' gradients. */
+ge_status_t ge_qk_backward(ge_qk_handle_t handle, const ge_qk_args_t* args, void* stream);
+void ge_qk_destroy(ge_qk_handle_t handle);
+
+/* ---------------------------------------------------------------------------------------------
+ * Global gradient norm over many tensors, and clipping:
+ *
+ *   norm = sqrt(sum over all tensors of the sum of squares)      (64-bit sums in a fixed order)
+ *   out_t = in_t * min(1, max_norm / (norm + eps))               (fp32 product, one rounding)
+ *
+ * A NaN or infinite gradient makes the norm NaN or infinite, and the products what the formula
+ * gives (times NaN, or times 0).  Tensors are dense arrays of bf16 or fp32 values (mixed freely),
+ * any length including 0, aligned to their elements.  out_t may be in_t (in place; nothing is
+ * written when the factor is 1); otherwise outputs must not overlap inputs or each other.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct {
+  int64_t numel;
+  int32_t dtype;                      /* GE_DT_BF16 or GE_DT_FP32 */
+} ge_clip_tensor_t;
+
+typedef struct {
+  const void* const* in;              /* host array of n device pointers, read during the call */
+  void* const* out;                   /* host array of n device pointers; NULL: only the norm */
+  float* norm;                        /* device, one float; may be NULL with out */
+  void* workspace;                    /* needs no zero fill */
+  size_t workspace_bytes;
+  float max_norm;                     /* >= 0 (may be infinite) */
+  float eps;                          /* finite, >= 0 */
+} ge_clip_args_t;
+
+typedef struct ge_clip_plan* ge_clip_handle_t;
+
+/* tensors: host array of n entries, copied into the handle.  GE_ERR_INVALID_ARG (n < 0, NULL with
+ * n > 0, a negative length, an unknown type), GE_ERR_UNSUPPORTED (2^46 values or more in all). */
+ge_status_t ge_clip_create(const ge_clip_tensor_t* tensors, int32_t n, ge_clip_handle_t* out);
+ge_status_t ge_clip_workspace_size(ge_clip_handle_t handle, size_t* bytes);
+/* Two launches for up to 128 non-empty tensors (one more pair for each further 128). */
+ge_status_t ge_clip_run(ge_clip_handle_t handle, const ge_clip_args_t* args, void* stream);
+void ge_clip_destroy(ge_clip_handle_t handle);
+
 #ifdef __cplusplus
 }
 #endif

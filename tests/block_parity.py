@@ -111,3 +111,54 @@ def check(got, ref, tol, what):
         i = int(torch.nan_to_num(off / tol, nan=math.inf).flatten().argmax())
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside; worst at {i}: got "
                              f"{float(got.double().flatten()[i])}, want {float(ref.flatten()[i])} +- {float(tol.flatten()[i])}")
+
+
+# ---- query/key norm with rotation ----
+# The angle is reduced to a turn in 64 bits and rounded once to fp32 (2^-25 of a turn, 2^-22.3 rad); its
+# cosine and sine add two units of 2^-24: ANGLE bounds the error of either.
+ANGLE = 2.0 ** -21
+
+
+def _turned(a, b, cos, sin):
+    return a * cos - b * sin, b * cos + a * sin
+
+
+def qk(x, dout, gain, pos, inv, amplitude, rot, pairs, eps):
+    """64-bit (out, tol) of one of queries or keys, or with dout (dx, tol, dgain, tol of dgain)."""
+    T, H, D = x.shape
+    x, half = x.double(), U if x.dtype == torch.bfloat16 else E
+    first = torch.arange(rot // 2, device=x.device) if pairs == "half" else torch.arange(0, rot, 2, device=x.device)
+    second = first + (rot // 2 if pairs == "half" else 1)
+    angle = pos.double()[:, None] * inv.double()[None, :]
+    cos, sin = amplitude * torch.cos(angle)[:, None], amplitude * torch.sin(angle)[:, None]
+    steps = (D + 16) * E
+
+    def rotate(v, s):
+        y = v.clone()
+        y[..., first], y[..., second] = _turned(v[..., first], v[..., second], cos, s)
+        size = v.abs()
+        both = abs(amplitude) * (v[..., first].abs() + v[..., second].abs())
+        size[..., first], size[..., second] = both, both
+        return y, size
+    r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) if gain is not None else None
+    if dout is None:
+        y = x * r * gain.double() if gain is not None else x
+        out, size = rotate(y, sin)
+        return out, half * out.abs() + (1 + half) * size * (ANGLE + steps) + TINY
+    dy, size = rotate(dout.double(), -sin)
+    tdy = size * (ANGLE + 4 * E)
+    if gain is None:
+        return dy, half * dy.abs() + (1 + half) * tdy + TINY, None, None
+    n, g = x * r, gain.double()
+    e, te = dy * g, tdy * g.abs() + steps * (dy * g).abs()
+    mean = (e * n).mean(-1, keepdim=True)
+    tmean = (te * n.abs()).mean(-1, keepdim=True) + steps * (e * n).abs().mean(-1, keepdim=True)
+    dx = r * (e - n * mean)
+    tdx = r * (te + n.abs() * tmean + 2 * steps * (e.abs() + (n * mean).abs()))
+    dgain = (dy * n).sum((0, 1))
+    tgain = (tdy * n.abs() + (steps + (T * H + 16) * E) * (dy * n).abs()).sum((0, 1))
+    return dx, half * dx.abs() + (1 + half) * tdx + TINY, dgain, tgain + E * dgain.abs() + TINY
+
+
+def half_step(dtype):
+    return U if dtype == torch.bfloat16 else E

@@ -1,0 +1,165 @@
+"""libge_block.so on the host: it loads, exports every symbol its header declares, and its HIP-free
+validation accepts and refuses as documented.  No compute is launched here."""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import gemm_epilogue_transformer_tiled_amd as ge
+from gemm_epilogue_transformer_tiled_amd import block
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_library_exports_every_declared_symbol():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "ge_block.h")).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(ge_(?:ffn|qk|clip)_\w+)\s*\(", text)))
+    lib = ctypes.CDLL(block.LIB_PATH)
+    for n in names:
+        assert hasattr(lib, n), n
+    assert set(names) == set(block.EXPORTED)
+
+
+def _ffn(**kw):
+    base = dict(M=64, d=64, h=128)
+    base.update(kw)
+    return block.lib.ge_ffn_validate(ctypes.byref(block.make_ffn_desc(**base)))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), ge.GE_OK),
+    (dict(M=0), ge.GE_OK),
+    (dict(M=1, h=0), ge.GE_OK),
+    (dict(M=777, d=8, h=8, w_layout="nk", act="none"), ge.GE_OK),
+    (dict(M=-1), ge.GE_ERR_INVALID_ARG),
+    (dict(d=-8), ge.GE_ERR_INVALID_ARG),
+    (dict(ldx=56), ge.GE_ERR_INVALID_ARG),            # below a row of X
+    (dict(ldw=120), ge.GE_ERR_INVALID_ARG),
+    (dict(ldw=64), ge.GE_ERR_INVALID_ARG),            # enough for [out][in] rows, not for [in][out]
+    (dict(ldw=64, w_layout="nk"), ge.GE_OK),
+    (dict(lddwd=56), ge.GE_ERR_INVALID_ARG),
+    (dict(d=60), ge.GE_ERR_UNSUPPORTED),
+    (dict(h=132), ge.GE_ERR_UNSUPPORTED),
+    (dict(ldg=132), ge.GE_ERR_UNSUPPORTED),
+    (dict(ldx=1 << 22), ge.GE_ERR_UNSUPPORTED),
+    (dict(M=1 << 31), ge.GE_ERR_UNSUPPORTED),
+    (dict(M=(1 << 31) - 1024, h=1 << 20), ge.GE_ERR_UNSUPPORTED),   # the grid passes 31 bits
+    (dict(tile=3), ge.GE_ERR_INVALID_ARG),
+])
+def test_ffn_descriptors(kw, want):
+    assert _ffn(**kw) == want
+
+
+@pytest.mark.parametrize("field,value", [("act", 4), ("act", -1), ("w_layout", 2), ("residual", 2), ("save", -1),
+                                         ("tile", -1)])
+def test_ffn_unknown_values(field, value):
+    d = block.make_ffn_desc(8, 8, 8)
+    setattr(d, field, value)
+    assert block.lib.ge_ffn_validate(ctypes.byref(d)) == ge.GE_ERR_INVALID_ARG
+
+
+def _qk(tokens=10, hq=4, hk=2, D=64, rot=None, **kw):
+    rot = D if rot is None else rot
+    d = block.ge_qk_desc_t(tokens, hq, hk, hq * D, D, hk * D, D, hq * D, D, hk * D, D, hq * D, D, hk * D, D, D, rot, 1, 1,
+                           ge.GE_DT_BF16, 1, 1e-6)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return block.lib.ge_qk_validate(ctypes.byref(d))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), ge.GE_OK),
+    (dict(tokens=0), ge.GE_OK),
+    (dict(hq=0), ge.GE_OK),
+    (dict(rot=0), ge.GE_OK),
+    (dict(D=20, rot=6), ge.GE_OK),
+    (dict(q_token=0, q_head=0), ge.GE_OK),              # an input may repeat
+    (dict(tokens=-1), ge.GE_ERR_INVALID_ARG),
+    (dict(rot=66), ge.GE_ERR_INVALID_ARG),
+    (dict(rot=-2), ge.GE_ERR_INVALID_ARG),
+    (dict(oq_token=0), ge.GE_ERR_INVALID_ARG),          # outputs may not
+    (dict(oq_head=32), ge.GE_ERR_INVALID_ARG),
+    (dict(dk_token=64), ge.GE_ERR_INVALID_ARG),         # two heads of 64 in 64
+    (dict(oq_token=64, oq_head=640), ge.GE_OK),         # [heads][tokens]
+    (dict(oq_token=64, oq_head=639), ge.GE_ERR_INVALID_ARG),
+    (dict(q_token=-1), ge.GE_ERR_INVALID_ARG),
+    (dict(pairs=2), ge.GE_ERR_INVALID_ARG),
+    (dict(norm=2), ge.GE_ERR_INVALID_ARG),
+    (dict(dtype=7), ge.GE_ERR_INVALID_ARG),
+    (dict(eps=-1e-6), ge.GE_ERR_INVALID_ARG),
+    (dict(eps=math.nan), ge.GE_ERR_INVALID_ARG),
+    (dict(eps=math.inf), ge.GE_ERR_INVALID_ARG),
+    (dict(dtype=ge.GE_DT_FP8_E4M3), ge.GE_ERR_UNSUPPORTED),
+    (dict(D=63, rot=62), ge.GE_ERR_UNSUPPORTED),
+    (dict(D=64, rot=63), ge.GE_ERR_UNSUPPORTED),
+    (dict(D=514), ge.GE_ERR_UNSUPPORTED),
+    (dict(tokens=1 << 41, q_token=1 << 20), ge.GE_ERR_UNSUPPORTED),
+])
+def test_qk_descriptors(kw, want):
+    assert _qk(**kw) == want
+
+
+def test_null_handles_and_arguments():
+    lib = block.lib
+    n = ctypes.c_size_t()
+    for name in ("ge_ffn", "ge_qk", "ge_clip"):
+        if name != "ge_clip":
+            assert getattr(lib, name + "_validate")(None) == ge.GE_ERR_INVALID_ARG
+            assert getattr(lib, name + "_create")(None, None) == ge.GE_ERR_INVALID_ARG
+        getattr(lib, name + "_destroy")(None)
+    assert lib.ge_ffn_workspace_size(None, 0, ctypes.byref(n)) == ge.GE_ERR_INVALID_ARG
+    assert lib.ge_qk_workspace_size(None, ctypes.byref(n)) == ge.GE_ERR_INVALID_ARG
+    assert lib.ge_clip_workspace_size(None, ctypes.byref(n)) == ge.GE_ERR_INVALID_ARG
+    for f in (lib.ge_ffn_forward, lib.ge_ffn_backward, lib.ge_qk_forward, lib.ge_qk_backward, lib.ge_clip_run):
+        assert f(None, None, None) == ge.GE_ERR_INVALID_ARG
+    out = ctypes.c_void_p(5)
+    assert lib.ge_clip_create(None, 3, ctypes.byref(out)) == ge.GE_ERR_INVALID_ARG and not out.value
+    bad = (block.ge_clip_tensor_t * 1)((-1, ge.GE_DT_BF16))
+    assert lib.ge_clip_create(bad, 1, ctypes.byref(out)) == ge.GE_ERR_INVALID_ARG
+    bad = (block.ge_clip_tensor_t * 1)((4, 9))
+    assert lib.ge_clip_create(bad, 1, ctypes.byref(out)) == ge.GE_ERR_INVALID_ARG
+    bad = (block.ge_clip_tensor_t * 1)((4, ge.GE_DT_FP8_E4M3))
+    assert lib.ge_clip_create(bad, 1, ctypes.byref(out)) == ge.GE_ERR_UNSUPPORTED
+    bad = (block.ge_clip_tensor_t * 2)((1 << 62, ge.GE_DT_BF16), (1 << 62, ge.GE_DT_BF16))
+    assert lib.ge_clip_create(bad, 2, ctypes.byref(out)) == ge.GE_ERR_UNSUPPORTED
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the refusal without a device")
+def test_no_device():
+    d = block.make_ffn_desc(8, 8, 8)
+    out = ctypes.c_void_p(5)
+    assert block.lib.ge_ffn_create(ctypes.byref(d), ctypes.byref(out)) == ge.GE_ERR_DEVICE and not out.value
+    t = (block.ge_clip_tensor_t * 1)((4, ge.GE_DT_BF16))
+    assert block.lib.ge_clip_create(t, 1, ctypes.byref(out)) == ge.GE_ERR_DEVICE
+
+
+def test_descriptor_helpers_refuse():
+    with pytest.raises(KeyError):
+        block.make_ffn_desc(8, 8, 8, act="tanh")
+    with pytest.raises(TypeError):
+        block.make_ffn_desc(8, 8, 8, ldq=8)
+    with pytest.raises(ValueError):
+        block.make_clip_args([torch.zeros(2)], [])
+
+
+def test_rotary_frequencies():
+    inv, amp = block.rotary_frequencies(8)
+    assert amp == 1.0 and torch.allclose(inv, torch.tensor([1.0, 0.1, 0.01, 0.001]))
+    lin, _ = block.rotary_frequencies(8, scaling="linear", factor=4.0)
+    assert torch.allclose(lin, inv / 4)
+    base, _ = block.rotary_frequencies(8, scaling="base", factor=4.0)
+    assert torch.allclose(base[0], inv[0]) and torch.allclose(base[-1], inv[-1] / 4)
+    part, amp = block.rotary_frequencies(128, scaling="by_parts", factor=8.0)
+    plain, _ = block.rotary_frequencies(128)
+    assert amp == pytest.approx(0.1 * math.log(8) + 1)
+    assert torch.equal(part[0], plain[0]) and torch.allclose(part[-1], plain[-1] / 8)
+    assert ((part <= plain) & (part >= plain / 8 * 0.999999)).all()
+    assert block.rotary_frequencies(0)[0].numel() == 0
+    for bad in (dict(rot_dim=7), dict(rot_dim=8, factor=0.5), dict(rot_dim=8, factor=math.inf), dict(rot_dim=8, scaling="x")):
+        with pytest.raises(ValueError):
+            block.rotary_frequencies(**bad)
