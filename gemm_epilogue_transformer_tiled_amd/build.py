@@ -20,7 +20,7 @@ ONE_WAVE = [f"ge_tile_{t}_{lay}.hip" for t in ("256x256", "256x128_pair", "128x1
             for lay in ("kn", "nk", "f8")]
 TWO_WAVE = [f"ge_tile_{t}_{lay}.hip" for t in ("256x256w8", "256x128w8_pair") for lay in ("kn", "nk", "f8")]
 COMMON = ["ge_kernels.hip", "noalloc.hip", "tiles.cpp", "api.cpp"]
-BLOCK = ["ge_ffn_pair.hip", "ge_ffn_grad.hip", "ge_ffn_plain.hip", "ge_qk.hip", "ge_clip.hip", "block_api.cpp",
+BLOCK = ["ge_ffn_pair.hip", "ge_ffn_grad.hip", "ge_ffn_plain.hip", "ge_ffn_few.hip", "ge_qk.hip", "ge_clip.hip", "block_api.cpp",
          "block_rowwise_api.cpp"]
 # library -> (its sources, extra compiler flags)
 TARGETS = {

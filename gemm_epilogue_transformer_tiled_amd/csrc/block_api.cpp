@@ -2,6 +2,8 @@
 // backward / destroy.  Host code only; the handle holds host memory only.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <new>
 
@@ -12,7 +14,7 @@
 struct ge_ffn_plan {
   ge_ffn_desc_t desc;
   int device;
-  int tile_pair, tile_down, tile_grad, tile_dx, tile_dw;   // ge::FfnTile per product
+  struct Choice { int tile, splits; } pair, down, grad, dx, dw;   // ge::FfnTile and splits per product
 };
 
 namespace {
@@ -30,22 +32,52 @@ constexpr int64_t kMaxSize = 0x7FFFFFFF - 512;
 // A row operand's buffer spans up to 256 rows of one leading dimension in 31-bit byte offsets.
 constexpr int64_t kMaxLd = int64_t(1) << 22;
 
-// Tile of one product by its grid: the largest tile that still gives `want` workgroups, so that
-// all 256 compute units have work (the 64-row tiles run several workgroups per unit).
-int pick_tile(int64_t M, int64_t N, bool pair, int32_t asked) {
-  if (asked) return asked - 1;
-  for (int t : {ge::FFN_T256, ge::FFN_T128}) {
+// Rows up to which the forward products run split over the contraction instead of in tiles.
+constexpr int64_t kFewRows = 32;
+// A tile's contraction is split over at most this many workgroups, and only in launches of at most
+// this many in all (three on every compute unit).
+constexpr int kMaxSplits = 16;
+constexpr int kMaxSplitGroups = 768;
+
+// Tile and splits of one launch: the least estimated time.  A workgroup of a tile needs `slot` us
+// for 64 values of the contraction and `fixed` us around them; `per_cu` of them share a compute
+// unit's time beyond the first.  A split adds the partial sums' way through memory.  The figures
+// are measured (ge_ffn_impl.h); they need only rank the choices.
+using Choice = ge_ffn_plan::Choice;
+Choice pick(int mode, int64_t M, int64_t N, int64_t K, int products, int32_t asked) {
+  if (asked) return Choice{asked - 1, 1};
+  const bool pair = mode == ge::FFN_PAIR;
+  const int64_t slots = ceil_div(K, 64) * (mode == ge::FFN_DUAL ? 2 : 1);
+  struct Cost { double fixed, slot, crowd; };           // crowd: a slot with several workgroups per CU, each
+  const Cost cost[ge::FFN_TILES] = {{12.0, 1.4, 1.4}, {6.0, pair ? 1.0 : 0.5, pair ? 1.0 : 0.55},
+                                    {4.5, pair ? 0.45 : 0.26, pair ? 0.43 : 0.21}};
+  Choice best{ge::FFN_T64, 1};
+  double least = 1e300;
+  for (int t = 0; t < ge::FFN_TILES; ++t) {
     const ge::FfnTileInfo ti = ge::ffn_tile_info(t);
-    if (ceil_div(M, ti.bm) * ceil_div(N, pair ? ti.bn_pair : ti.bn) >= 192) return t;
+    const int bn = pair ? ti.bn_pair : ti.bn;
+    const double tiles = (double)ceil_div(M, ti.bm) * (double)ceil_div(N, bn) * products;
+    for (int s = 1; s <= (t == ge::FFN_T256 ? 1 : kMaxSplits); s *= 2) {
+      if (s > 1 && (slots < 4 * s || tiles * s > kMaxSplitGroups)) break;
+      const double rounds = std::ceil(tiles * s / 256.0), mine = (double)ceil_div(slots, s);
+      double us = cost[t].fixed + mine * (rounds > 1 ? rounds * cost[t].crowd : cost[t].slot);
+      if (s > 1) us += 2.5 + tiles * s * ti.bm * bn * (pair ? 8.0 : 4.0) * 2 / 3e6;
+      if (us < least) {
+        least = us;
+        best = Choice{t, s};
+      }
+    }
   }
-  return ge::FFN_T64;
+  return best;
 }
 
 // Adds a product to a launch; returns false if the grid would pass 31 bits.
-bool add(ge::FfnLaunch& l, ge::FfnProduct p, int tile, bool pair) {
+bool add(ge::FfnLaunch& l, ge::FfnProduct p, const Choice& c, bool pair) {
+  const int tile = c.tile;
+  l.splits = c.splits;
   const ge::FfnTileInfo ti = ge::ffn_tile_info(tile);
   const int64_t tm = ceil_div(p.M, ti.bm), tn = ceil_div(p.N, pair ? ti.bn_pair : ti.bn);
-  if (l.tiles + tm * tn > 0x7FFFFFFF) return false;
+  if ((l.tiles + tm * tn) * c.splits > 0x7FFFFFFF) return false;
   p.tiles_m = (int32_t)tm;
   p.tiles_n = (int32_t)tn;
   p.tile0 = l.tiles;
@@ -54,11 +86,72 @@ bool add(ge::FfnLaunch& l, ge::FfnProduct p, int tile, bool pair) {
   return true;
 }
 
+// Few rows: how a product is split.  Row groups of 16 or 32 rows; one workgroup of eight waves on
+// every compute unit at most, and no more splits than the longest wave's share needs.
+struct FewPlan { int rows, row_groups, tiles, splits; };
+FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
+  FewPlan f;
+  f.rows = M <= 16 ? 16 : 32;
+  f.row_groups = (int)ceil_div(M, f.rows);
+  f.tiles = (int)ceil_div(N, ge::kFfnFewCols);
+  const int64_t units = ceil_div(K, ge::kFfnFewUnit), waves = 8;
+  const int64_t most = std::max<int64_t>(1, 256 / std::max<int64_t>((int64_t)f.tiles * f.row_groups, 1));
+  const int64_t share = std::max<int64_t>(1, ceil_div(units, waves * most));     // units of the longest wave
+  f.splits = (int)std::max<int64_t>(1, ceil_div(units, waves * share));
+  return f;
+}
+size_t few_ctr_bytes(const FewPlan& f) { return (size_t)f.tiles * f.row_groups * ge::kFfnCtrStride * 4; }
+size_t few_part_bytes(const FewPlan& f, int operands) {
+  return f.splits > 1 ? (size_t)f.tiles * f.row_groups * f.splits * operands * f.rows * ge::kFfnFewCols * 4 : 0;
+}
+
 size_t hidden_bytes(const ge_ffn_desc_t& d) { return (size_t)d.M * (size_t)d.h * 2; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-size_t forward_bytes(const ge_ffn_plan* p) { return round256(hidden_bytes(p->desc)); }
-size_t backward_bytes(const ge_ffn_plan* p) { return 3 * round256(hidden_bytes(p->desc)); }
+// Workspace of both calls: [tickets][partial sums][H], or [tickets][partial sums][dG][dU][H].  The
+// tickets come first and take the same room in both, so one workspace may serve both in turn; the
+// launches of a call follow each other and use the tickets and the partial sums in turn.
+struct Layout { size_t part, hidden, total; };
+bool few_rows(const ge_ffn_desc_t& d) { return d.tile == 0 && d.M <= kFewRows && d.d > 0 && d.h > 0; }
+FewPlan few_up(const ge_ffn_desc_t& d) { return few_plan(d.M, d.h, d.d); }
+FewPlan few_down(const ge_ffn_desc_t& d) { return few_plan(d.M, d.d, d.h); }
+size_t ticket_bytes(const ge_ffn_desc_t& d) {
+  size_t b = (size_t)kMaxSplitGroups * ge::kFfnCtrStride * 4;
+  if (few_rows(d)) b = std::max({b, few_ctr_bytes(few_up(d)), few_ctr_bytes(few_down(d))});
+  return round256(b);
+}
+size_t part_bytes(const Choice& c, int64_t M, int64_t N, bool pair, int products = 1) {
+  if (c.splits < 2) return 0;
+  const ge::FfnTileInfo ti = ge::ffn_tile_info(c.tile);
+  const int bn = pair ? ti.bn_pair : ti.bn;
+  return (size_t)(ceil_div(M, ti.bm) * ceil_div(N, bn) * products) * c.splits * ti.bm * bn * (pair ? 8 : 4);
+}
+Layout forward_layout(const ge_ffn_plan* p) {
+  const ge_ffn_desc_t& d = p->desc;
+  Layout l{};
+  l.part = ticket_bytes(d);
+  const size_t sums = few_rows(d) ? std::max(few_part_bytes(few_up(d), 2), few_part_bytes(few_down(d), 1))
+                                  : std::max(part_bytes(p->pair, d.M, d.h, true), part_bytes(p->down, d.M, d.d, false));
+  l.hidden = l.part + round256(sums);
+  l.total = l.hidden + round256(hidden_bytes(d));
+  return l;
+}
+Layout backward_layout(const ge_ffn_plan* p) {
+  const ge_ffn_desc_t& d = p->desc;
+  Layout l{};
+  l.part = ticket_bytes(d);
+  l.hidden = l.part + round256(std::max({part_bytes(p->grad, d.M, d.h, false), part_bytes(p->dx, d.M, d.d, false),
+                                         part_bytes(p->dw, d.d, d.h, false, 3)}));
+  l.total = l.hidden + 3 * round256(hidden_bytes(d));
+  return l;
+}
+size_t forward_bytes(const ge_ffn_plan* p) { return forward_layout(p).total; }
+size_t backward_bytes(const ge_ffn_plan* p) { return backward_layout(p).total; }
+// Points a launch at the workspace's tickets and partial sums.
+void share(ge::FfnLaunch& l, unsigned char* ws, const Layout& lay) {
+  l.ctr = reinterpret_cast<uint32_t*>(ws);
+  l.part = reinterpret_cast<float*>(ws + lay.part);
+}
 
 Matrix weight_in(const ge_ffn_desc_t& d, const void* p, int64_t ld) {      // Wg, Wu and their gradients
   return d.w_layout == GE_LAYOUT_KN ? Matrix{p, d.d, d.h, ld} : Matrix{p, d.h, d.d, ld};
@@ -109,11 +202,11 @@ ge_status_t ge_ffn_create(const ge_ffn_desc_t* d, ge_ffn_handle_t* handle) {
   if (!p) return GE_ERR_HIP;
   p->desc = *d;
   p->device = device;
-  p->tile_pair = pick_tile(d->M, d->h, true, d->tile);
-  p->tile_down = pick_tile(d->M, d->d, false, d->tile);
-  p->tile_grad = pick_tile(d->M, d->h, false, d->tile);
-  p->tile_dx = pick_tile(d->M, d->d, false, d->tile);
-  p->tile_dw = pick_tile(d->d, 3 * d->h, false, d->tile);
+  p->pair = pick(ge::FFN_PAIR, d->M, d->h, d->d, 1, d->tile);
+  p->down = pick(ge::FFN_DOWN, d->M, d->d, d->h, 1, d->tile);
+  p->grad = pick(ge::FFN_GRAD, d->M, d->h, d->d, 1, d->tile);
+  p->dx = pick(ge::FFN_DUAL, d->M, d->d, d->h, 1, d->tile);
+  p->dw = pick(ge::FFN_WGRAD, d->d, d->h, d->M, 3, d->tile);
   *handle = p;
   return GE_OK;
 }
@@ -129,9 +222,12 @@ ge_status_t ge_ffn_workspace_size(ge_ffn_handle_t h, int32_t backward, size_t* b
 ge_status_t ge_ffn_describe(ge_ffn_handle_t h, char* buf, size_t len) {
   if (!h || !buf || len == 0) return GE_ERR_INVALID_ARG;
   const int rows[] = {256, 128, 64};
-  std::snprintf(buf, len, "pair=%d down=%d grad=%d dx=%d dw=%d b=%s act=%d", rows[h->tile_pair], rows[h->tile_down],
-                rows[h->tile_grad], rows[h->tile_dx], rows[h->tile_dw], h->desc.w_layout == GE_LAYOUT_NK ? "NK" : "KN",
-                (int)h->desc.act);
+  char up[32];
+  if (few_rows(h->desc)) std::snprintf(up, sizeof up, "few rows");
+  else std::snprintf(up, sizeof up, "pair=%d/%d down=%d/%d", rows[h->pair.tile], h->pair.splits, rows[h->down.tile], h->down.splits);
+  std::snprintf(buf, len, "%s grad=%d/%d dx=%d/%d dw=%d/%d b=%s act=%d", up, rows[h->grad.tile], h->grad.splits,
+                rows[h->dx.tile], h->dx.splits, rows[h->dw.tile], h->dw.splits,
+                h->desc.w_layout == GE_LAYOUT_NK ? "NK" : "KN", (int)h->desc.act);
   return GE_OK;
 }
 
@@ -151,22 +247,45 @@ ge_status_t ge_ffn_forward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* stre
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool nk = d.w_layout == GE_LAYOUT_NK;
-  uint16_t* H = out(a->workspace);
+  const Layout lay = forward_layout(h);
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  uint16_t* H = out(ws + lay.hidden);
+  if (few_rows(d)) {
+    FewPlan f = few_up(d);
+    ge::FfnFew q{};
+    q.A = in(a->X); q.B = in(a->Wg); q.B2 = in(a->Wu);
+    q.Y = H; q.Y2 = d.save ? out(a->G) : nullptr; q.Y3 = d.save ? out(a->U) : nullptr;
+    q.part = reinterpret_cast<float*>(ws + lay.part); q.ctr = reinterpret_cast<uint32_t*>(ws);
+    q.lda = d.ldx; q.ldb = d.ldw; q.ldy = d.h; q.ldy2 = d.ldg;
+    q.M = (int32_t)d.M; q.N = (int32_t)d.h; q.K = (int32_t)d.d;
+    q.tiles = f.tiles; q.splits = f.splits; q.rows = f.rows; q.row_groups = f.row_groups;
+    if (ge::launch_ffn_few(true, d.act, nk, q, s) != hipSuccess) return GE_ERR_HIP;
+    f = few_down(d);
+    q = ge::FfnFew{};
+    q.A = H; q.B = in(a->Wd); q.E1 = d.residual ? in(a->residual) : nullptr; q.Y = out(a->Y);
+    q.part = reinterpret_cast<float*>(ws + lay.part); q.ctr = reinterpret_cast<uint32_t*>(ws);
+    q.lda = d.h; q.ldb = d.ldwd; q.lde = d.ldr; q.ldy = d.ldy;
+    q.M = (int32_t)d.M; q.N = (int32_t)d.d; q.K = (int32_t)d.h;
+    q.tiles = f.tiles; q.splits = f.splits; q.rows = f.rows; q.row_groups = f.row_groups;
+    return ge::launch_ffn_few(false, ge::ACT_NONE, nk, q, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
+  }
   ge::FfnLaunch pair{}, down{};
   ge::FfnProduct p{};
   p.A = in(a->X); p.B = in(a->Wg); p.B2 = in(a->Wu);
   p.Y = H; p.Y2 = d.save ? out(a->G) : nullptr; p.Y3 = d.save ? out(a->U) : nullptr;
   p.lda = d.ldx; p.ldb = d.ldw; p.ldy = d.h; p.ldy2 = d.ldg;
   p.M = (int32_t)d.M; p.N = (int32_t)d.h; p.K = (int32_t)d.d;
-  if (!add(pair, p, h->tile_pair, true)) return GE_ERR_UNSUPPORTED;
+  if (!add(pair, p, h->pair, true)) return GE_ERR_UNSUPPORTED;
   p = ge::FfnProduct{};
   p.A = H; p.B = in(a->Wd); p.E1 = d.residual ? in(a->residual) : nullptr;
   p.Y = out(a->Y);
   p.lda = d.h; p.ldb = d.ldwd; p.lde = d.ldr; p.ldy = d.ldy;
   p.M = (int32_t)d.M; p.N = (int32_t)d.d; p.K = (int32_t)d.h;
-  if (!add(down, p, h->tile_down, false)) return GE_ERR_UNSUPPORTED;
-  if (ge::launch_ffn_pair(h->tile_pair, d.act, nk, pair, s) != hipSuccess) return GE_ERR_HIP;
-  if (ge::launch_ffn_plain(ge::FFN_DOWN, h->tile_down, nk, down, s) != hipSuccess) return GE_ERR_HIP;
+  if (!add(down, p, h->down, false)) return GE_ERR_UNSUPPORTED;
+  share(pair, ws, lay);
+  share(down, ws, lay);
+  if (ge::launch_ffn_pair(h->pair.tile, d.act, nk, pair, s) != hipSuccess) return GE_ERR_HIP;
+  if (ge::launch_ffn_plain(ge::FFN_DOWN, h->down.tile, nk, down, s) != hipSuccess) return GE_ERR_HIP;
   return GE_OK;
 }
 
@@ -185,14 +304,16 @@ ge_status_t ge_ffn_backward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* str
   const Matrix outputs[] = {{a->dX, rows_dx, d.d, d.lddx},
                             want_dw ? weight_in(d, a->dWg, d.lddw) : none, want_dw ? weight_in(d, a->dWu, d.lddw) : none,
                             want_dw ? weight_out(d, a->dWd, d.lddwd) : none,
-                            {a->workspace, 1, (int64_t)(3 * hb / 2), (int64_t)(3 * hb / 2)}};
+                            {a->workspace, 1, (int64_t)(backward_bytes(h) / 2), (int64_t)(backward_bytes(h) / 2)}};
   if (!ge::block::usable(inputs, 7, outputs, 5, -1, -1)) return GE_ERR_INVALID_ARG;
   if (a->workspace_bytes < backward_bytes(h)) return GE_ERR_INVALID_ARG;
   if (!ge::block::is_current(h->device)) return GE_ERR_DEVICE;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool nk = d.w_layout == GE_LAYOUT_NK;
-  uint16_t* dG = out(a->workspace);
+  const Layout lay = backward_layout(h);
+  unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+  uint16_t* dG = out(ws + lay.hidden);
   uint16_t* dU = dG + hb / 2;
   uint16_t* H = dU + hb / 2;
   ge::FfnLaunch grad{}, dx{}, dw{};
@@ -202,13 +323,13 @@ ge_status_t ge_ffn_backward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* str
   p.Y = dG; p.Y2 = dU; p.Y3 = H;
   p.lda = d.lddy; p.ldb = d.ldwd; p.lde = d.ldg; p.ldy = d.h; p.ldy2 = d.h;
   p.M = (int32_t)d.M; p.N = (int32_t)d.h; p.K = (int32_t)d.d;
-  if (!add(grad, p, h->tile_grad, false)) return GE_ERR_UNSUPPORTED;
+  if (!add(grad, p, h->grad, false)) return GE_ERR_UNSUPPORTED;
   if (want_dx) {
     p = ge::FfnProduct{};
     p.A = dG; p.A2 = dU; p.B = in(a->Wg); p.B2 = in(a->Wu); p.Y = out(a->dX);
     p.lda = d.h; p.ldb = d.ldw; p.ldy = d.lddx;
     p.M = (int32_t)d.M; p.N = (int32_t)d.d; p.K = (int32_t)d.h;
-    if (!add(dx, p, h->tile_dx, false)) return GE_ERR_UNSUPPORTED;
+    if (!add(dx, p, h->dx, false)) return GE_ERR_UNSUPPORTED;
   }
   if (want_dw) {
     // contraction over the rows; [in][out] weights: X^T dG, X^T dU, H^T dY; [out][in]: swapped
@@ -222,12 +343,13 @@ ge_status_t ge_ffn_backward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* str
       p.lda = nk ? t.ldr : t.ldl; p.ldb = nk ? t.ldl : t.ldr;
       p.M = (int32_t)(nk ? t.n : t.m); p.N = (int32_t)(nk ? t.m : t.n); p.K = (int32_t)d.M;
       p.Y = out(t.y); p.ldy = t.ldy;
-      if (!add(dw, p, h->tile_dw, false)) return GE_ERR_UNSUPPORTED;
+      if (!add(dw, p, h->dw, false)) return GE_ERR_UNSUPPORTED;
     }
   }
-  if (ge::launch_ffn_grad(h->tile_grad, d.act, !nk, grad, s) != hipSuccess) return GE_ERR_HIP;
-  if (ge::launch_ffn_plain(ge::FFN_DUAL, h->tile_dx, !nk, dx, s) != hipSuccess) return GE_ERR_HIP;
-  if (ge::launch_ffn_plain(ge::FFN_WGRAD, h->tile_dw, false, dw, s) != hipSuccess) return GE_ERR_HIP;
+  for (ge::FfnLaunch* l : {&grad, &dx, &dw}) share(*l, ws, lay);
+  if (ge::launch_ffn_grad(h->grad.tile, d.act, !nk, grad, s) != hipSuccess) return GE_ERR_HIP;
+  if (ge::launch_ffn_plain(ge::FFN_DUAL, h->dx.tile, !nk, dx, s) != hipSuccess) return GE_ERR_HIP;
+  if (ge::launch_ffn_plain(ge::FFN_WGRAD, h->dw.tile, false, dw, s) != hipSuccess) return GE_ERR_HIP;
   return GE_OK;
 }
 

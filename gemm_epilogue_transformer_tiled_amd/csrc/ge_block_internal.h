@@ -29,13 +29,31 @@ constexpr int kFfnMaxProducts = 3;
 struct FfnLaunch {
   FfnProduct prod[kFfnMaxProducts];
   int32_t n, tiles;
+  int32_t splits;             // workgroups that share a tile's contraction (1 with the 256-row tiles)
+  float* part;                // splits > 1: partial sums [tile][split][bm * bn * operands]
+  uint32_t* ctr;              // splits > 1: tickets per tile, zero between calls
 };
+constexpr uint32_t kFfnCtrStride = 16;       // 64 bytes between tickets
 
 struct FfnTileInfo { int bm, bn, bn_pair; };
 inline FfnTileInfo ffn_tile_info(int tile) {
   return tile == FFN_T256 ? FfnTileInfo{256, 256, 128} : tile == FFN_T128 ? FfnTileInfo{128, 128, 128}
                                                                           : FfnTileInfo{64, 64, 64};
 }
+
+// Few rows: products split over the contraction (ge_ffn_few.hip).
+struct FfnFew {
+  const uint16_t *A, *B, *B2, *E1;
+  uint16_t *Y, *Y2, *Y3;
+  float* part;                        // [tile][row group][split][operand][rows][kFfnFewCols]
+  uint32_t* ctr;                      // tickets per tile and row group, zero between calls
+  int64_t lda, ldb, lde, ldy, ldy2;
+  int32_t M, N, K;
+  int32_t tiles, splits, rows, row_groups;   // rows of a row group: 16 or 32
+};
+constexpr int kFfnFewCols = 128;
+constexpr int kFfnFewUnit = 64;              // K values a wave takes at a time
+hipError_t launch_ffn_few(bool pair, int act, bool b_nk, const FfnFew& p, hipStream_t s);
 
 // b_nk: B (and B2) given [N][K]; otherwise [K][N].  One translation unit per mode group.
 hipError_t launch_ffn_pair(int tile, int act, bool b_nk, const FfnLaunch& l, hipStream_t s);

@@ -31,10 +31,10 @@
 namespace ge {
 namespace {
 
-template <int BM_, int BN_, int NB_, int WAVES_, int NSLOT_>
+template <int BM_, int BN_, int NB_, int WAVES_, int NSLOT_, bool PP_ = false>
 struct FTile {
   static constexpr int BM = BM_, BN = BN_, NB = NB_, WAVES = WAVES_, NSLOT = NSLOT_;
-  static constexpr bool PP = WAVES == 8;              // two waves per SIMD, alternating phases
+  static constexpr bool PP = PP_;                     // two waves per SIMD, alternating phases
   static constexpr int NT = 64 * WAVES, WGN = WAVES / 2;
   static constexpr int WM = BM / 2, WN = BN / WGN;    // per-wave output: 2 x WGN waves
   static constexpr int FM = WM / 16, FN = WN / 16;
@@ -48,8 +48,8 @@ struct FTile {
   static constexpr int A_ALLOC = A_SLOT > WGN * EP_WAVE ? A_SLOT : WGN * EP_WAVE;
   static_assert(A_SLOT % (1024 * WAVES) == 0 && B_SLOT % (1024 * WAVES) == 0, "loads divide over the waves");
   static_assert(WM % 32 == 0 && WN % 16 == 0, "epilogue blocks");
-  static_assert(!PP || (NSLOT == 2 && LB % 2 == 0), "two-wave loop: two slots");
-  static_assert(NSLOT >= 2 && NSLOT <= 3, "slot arrays");
+  static_assert(!PP || (WAVES == 8 && NSLOT == 2 && LB % 2 == 0), "two-wave loop: two slots");
+  static_assert(NSLOT >= 2 && NSLOT <= 5, "slot arrays");
 };
 
 // Chunk swizzle of a column operand's staged row k (see swz_b16); rows of eight chunks have no
@@ -79,27 +79,35 @@ void ffn_product(FfnLaunch l) {
   static_assert((NB == 2) == PAIR, "two B operands: the gate/up pair");
   constexpr int BST = T::B_SLOT / 2;                   // 32-deep stage of B (two-wave loop, column B)
   constexpr int B01 = (T::PP && BC) ? BST : T::B_SLOT;
-  constexpr int B23 = (T::PP && BC) ? BST : (T::NSLOT > 2 ? T::B_SLOT : 16);
-  constexpr int A2B = T::NSLOT > 2 ? T::A_SLOT : 16;
+  constexpr int B2B = (T::PP && BC) ? BST : (T::NSLOT > 2 ? T::B_SLOT : 16);
+  constexpr int B3B = (T::PP && BC) ? BST : (T::NSLOT > 3 ? T::B_SLOT : 16);
+  constexpr int A2B = T::NSLOT > 2 ? T::A_SLOT : 16, A3B = T::NSLOT > 3 ? T::A_SLOT : 16;
+  constexpr int A4B = T::NSLOT > 4 ? T::A_SLOT : 16, B4B = T::NSLOT > 4 ? T::B_SLOT : 16;
   // distinct arrays: the compiler can tell that a load into one does not alias reads of another
   __shared__ __attribute__((aligned(1024))) unsigned char a0[T::A_ALLOC];
   __shared__ __attribute__((aligned(1024))) unsigned char a1[T::A_ALLOC];
   __shared__ __attribute__((aligned(1024))) unsigned char a2[A2B];
+  __shared__ __attribute__((aligned(1024))) unsigned char a3[A3B];
+  __shared__ __attribute__((aligned(1024))) unsigned char a4[A4B];
   __shared__ __attribute__((aligned(1024))) unsigned char b0[B01];
   __shared__ __attribute__((aligned(1024))) unsigned char b1[B01];
-  __shared__ __attribute__((aligned(1024))) unsigned char b2[B23];
-  __shared__ __attribute__((aligned(1024))) unsigned char b3[(T::PP && BC) ? BST : 16];
-  static_assert(2 * T::A_ALLOC + A2B + 2 * B01 + B23 + 4096 + BST <= 160 * 1024, "LDS of a workgroup");
+  __shared__ __attribute__((aligned(1024))) unsigned char b2[B2B];
+  __shared__ __attribute__((aligned(1024))) unsigned char b3[B3B];
+  __shared__ __attribute__((aligned(1024))) unsigned char b4[B4B];
+  static_assert(2 * T::A_ALLOC + A2B + A3B + A4B + 2 * B01 + B2B + B3B + B4B + 4096 <= 160 * 1024, "LDS of a workgroup");
   auto a_arr = [&](auto i) -> unsigned char* {
     if constexpr (decltype(i)::value == 0) return a0;
     else if constexpr (decltype(i)::value == 1) return a1;
-    else return a2;
+    else if constexpr (decltype(i)::value == 2) return a2;
+    else if constexpr (decltype(i)::value == 3) return a3;
+    else return a4;
   };
   auto b_arr = [&](auto i) -> unsigned char* {
     if constexpr (decltype(i)::value == 0) return b0;
     else if constexpr (decltype(i)::value == 1) return b1;
     else if constexpr (decltype(i)::value == 2) return b2;
-    else return b3;
+    else if constexpr (decltype(i)::value == 3) return b3;
+    else return b4;
   };
 #define GE_I(n) std::integral_constant<int, (n)>{}
 
@@ -111,13 +119,16 @@ void ffn_product(FfnLaunch l) {
   // ---- tile: contiguous runs per XCD (workgroups are dealt round-robin over the 8 dies), the
   // launch's products one after the other, tile rows walked in groups for L2 reuse ----
   int id;
+  const int splits = T::PP ? 1 : l.splits;
   {
-    const int total = l.tiles, x = (int)blockIdx.x % kXCDs, loc = (int)blockIdx.x / kXCDs;
+    const int total = l.tiles * splits, x = (int)blockIdx.x % kXCDs, loc = (int)blockIdx.x / kXCDs;
     const int per = (total + kXCDs - 1) / kXCDs;
     int tall = total % kXCDs;
     if (tall == 0) tall = kXCDs;
     id = x < tall ? x * per + loc : tall * per + (x - tall) * (per - 1) + loc;
   }
+  const int split = T::PP ? 0 : id / l.tiles, tile_id = id - split * l.tiles;
+  id = tile_id;
   int pi = 0;
   if (MODE == FFN_WGRAD) pi = (l.n > 1 && id >= l.prod[1].tile0) + (l.n > 2 && id >= l.prod[2].tile0);
   const FfnProduct& p = l.prod[pi];
@@ -133,6 +144,10 @@ void ffn_product(FfnLaunch l) {
   const int64_t a_at = AC ? (int64_t)m0 : (int64_t)m0 * p.lda, b_at = BC ? (int64_t)n0 : (int64_t)n0 * p.ldb;
   // contraction position of step j: DUAL runs through [0, K) twice, each pass padded to slots
   const int seg = 2 * ((K + 63) / 64);                 // steps of one pass, an even number
+  const int nk = (DUAL ? 2 : 1) * seg;                 // 32-deep steps; those past the end read zeros
+  // 64-deep slots of this workgroup's split
+  const int slot0 = T::PP ? 0 : (int)((int64_t)(nk / 2) * split / splits);
+  const int slot1 = T::PP ? nk / 2 : (int)((int64_t)(nk / 2) * (split + 1) / splits);
   auto second = [&](int j) { return DUAL && j >= seg; };
   auto kpos = [&](int j) { return (second(j) ? j - seg : j) * 32; };
   __amdgpu_buffer_rsrc_t ars, brs, brs2;
@@ -151,12 +166,12 @@ void ffn_product(FfnLaunch l) {
   };
   auto set_a = [&](int j) {
     const int k0 = kpos(j);
-    a_lim = K - k0;
+    a_lim = (T::PP || j < 2 * slot1) ? K - k0 : 0;
     ars = make_rsrc(at_k(AC, second(j) ? pa2 : pa, k0, lda2), extent(AC, a_lim, mrows, lda2));
   };
   auto set_b = [&](int j) {
     const int k0 = kpos(j);
-    b_lim = K - k0;
+    b_lim = (T::PP || j < 2 * slot1) ? K - k0 : 0;
     const int ext = extent(BC, b_lim, ncols, ldb2);
     brs = make_rsrc(at_k(BC, second(j) ? pb2 : pb, k0, ldb2), ext);
     if constexpr (PAIR) brs2 = make_rsrc(at_k(BC, pb2, k0, ldb2), ext);
@@ -264,13 +279,15 @@ void ffn_product(FfnLaunch l) {
     const v4bf16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf16*)(q + 4 * pitch));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  bf16x8_t fa[T::FM], fb[NB][T::FN];
+  struct Frags {
+    bf16x8_t a[T::FM], b[NB][T::FN];
+  };
   // fragments of one 32-deep step: half h of the slots, or (staged B) the whole stage
-  auto read_frags = [&](const unsigned char* as, const unsigned char* bs, int h) {
+  auto read_frags = [&](Frags& f, const unsigned char* as, const unsigned char* bs, int h) {
 #pragma unroll
     for (int i = 0; i < T::FM; ++i) {
-      if constexpr (AC) fa[i] = tr_read(as + ac[i] + h * 32 * (T::BM * 2), T::BM * 2);
-      else fa[i] = *(const bf16x8_t*)(as + ar[h][i & 1] + (i >> 1) * 32 * 128);
+      if constexpr (AC) f.a[i] = tr_read(as + ac[i] + h * 32 * (T::BM * 2), T::BM * 2);
+      else f.a[i] = *(const bf16x8_t*)(as + ar[h][i & 1] + (i >> 1) * 32 * 128);
     }
 #pragma unroll
     for (int op = 0; op < NB; ++op)
@@ -278,9 +295,9 @@ void ffn_product(FfnLaunch l) {
       for (int i = 0; i < T::FN; ++i) {
         if constexpr (BC) {
           constexpr int opb = BSTAGE ? T::B_OP / 2 : T::B_OP;
-          fb[op][i] = tr_read(bs + bc[i] + op * opb + (BSTAGE ? 0 : h * 32 * (T::BN * 2)), T::BN * 2);
+          f.b[op][i] = tr_read(bs + bc[i] + op * opb + (BSTAGE ? 0 : h * 32 * (T::BN * 2)), T::BN * 2);
         } else {
-          fb[op][i] = *(const bf16x8_t*)(bs + br[h][i & 1] + (i >> 1) * 32 * 128 + op * T::B_OP);
+          f.b[op][i] = *(const bf16x8_t*)(bs + br[h][i & 1] + (i >> 1) * 32 * 128 + op * T::B_OP);
         }
       }
   };
@@ -292,14 +309,14 @@ void ffn_product(FfnLaunch l) {
     for (int i = 0; i < T::FN; ++i)
 #pragma unroll
       for (int j = 0; j < T::FM; ++j) acc[op][i][j] = f32x4_t{};
-  auto mfmas = [&]() {
+  auto mfmas = [&](const Frags& f) {
 #pragma unroll
     for (int i = 0; i < T::FN; ++i)
 #pragma unroll
       for (int j = 0; j < T::FM; ++j)
 #pragma unroll
         for (int op = 0; op < NB; ++op)
-          acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[op][i], fa[j], acc[op][i][j], 0, 0, 0);
+          acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[op][i], f.a[j], acc[op][i][j], 0, 0, 0);
   };
   // a workgroup barrier that no LDS access moves across (the waits are explicit)
   auto barrier = [] {
@@ -308,12 +325,12 @@ void ffn_product(FfnLaunch l) {
     asm volatile("" ::: "memory");
   };
 
-  const int nk = (DUAL ? 2 : 1) * seg;                 // 32-deep steps; those past the end read zeros
   if constexpr (T::PP) {
     // ---- two wave groups, one phase apart (ge_kernel_impl.h describes the phases) ----
     // Even steps j load the A slot of steps j+2, j+3; with a column B odd steps load its stages
     // of steps j+2, j+3, with a row B even steps load its slot along with A's.
     const int grp = wave >> 2;
+    Frags f;
     set_a(0);
     issue_a(a0);
     if constexpr (BC) {
@@ -347,7 +364,7 @@ void ffn_product(FfnLaunch l) {
         }
       };
       if constexpr (!BC) loads();
-      read_frags(as, bs, S % 2);
+      read_frags(f, as, bs, S % 2);
       if constexpr (BC) {
         __builtin_amdgcn_sched_barrier(0);
         loads();
@@ -360,7 +377,7 @@ void ffn_product(FfnLaunch l) {
     };
     auto mat_phase = [&]() {
       __builtin_amdgcn_s_setprio(1);
-      mfmas();
+      mfmas(f);
       __builtin_amdgcn_s_setprio(0);
       barrier();
     };
@@ -378,38 +395,98 @@ void ffn_product(FfnLaunch l) {
   } else {
     // ---- ring of NSLOT slots: slot s is read while s+1 .. s+NSLOT-1 are on their way ----
     constexpr int NS = T::NSLOT, L = T::LA + LBF;
-    const int ns = nk / 2;
     auto fill = [&](auto i_c, int s) {
       set_a(2 * s);
       issue_a(a_arr(i_c));
       set_b(2 * s);
       issue_b(b_arr(i_c));
     };
-    fill(GE_I(0), 0);
-    if constexpr (NS > 2) fill(GE_I(1), 1);
-    auto turn = [&](auto i_c, int s) {
-      constexpr int I = decltype(i_c)::value;
-      // slot s has landed (this wave's part), and this wave is done reading slot s-1: after the
-      // barrier both hold for every wave, so the array of slot s-1 may be refilled
+    fill(GE_I(0), slot0);
+    if constexpr (NS > 2) fill(GE_I(1), slot0 + 1);
+    if constexpr (NS > 3) fill(GE_I(2), slot0 + 2);
+    if constexpr (NS > 4) fill(GE_I(3), slot0 + 3);
+    // the next slot has landed (this wave's part) and this wave is done reading this one: after the
+    // barrier both hold for every wave, so the next slot may be read and this one refilled
+    auto next = [&]() {
       __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm((NS - 2) * L));
       barrier();
-      fill(GE_I((I + NS - 1) % NS), s + NS - 1);
-      read_frags(a_arr(GE_I(I)), b_arr(GE_I(I)), 0);
-      mfmas();
-      read_frags(a_arr(GE_I(I)), b_arr(GE_I(I)), 1);
-      mfmas();
     };
-    for (int s = 0; s < ns; s += NS) {
+    next();
+    // the fragments of a half are read while the other half's products run
+    Frags f0, f1;
+    read_frags(f0, a0, b0, 0);
+    auto turn = [&](auto i_c, int s) {
+      constexpr int I = decltype(i_c)::value;
+      fill(GE_I((I + NS - 1) % NS), s + NS - 1);
+      read_frags(f1, a_arr(GE_I(I)), b_arr(GE_I(I)), 1);
+      mfmas(f0);
+      next();
+      read_frags(f0, a_arr(GE_I((I + 1) % NS)), b_arr(GE_I((I + 1) % NS)), 0);
+      mfmas(f1);
+    };
+    // Whole rings (slots past the end read zeros): with an exit after every slot the compiler saw paths
+    // on which a slot is read right after its loads were issued, and waited for all loads each ring.
+    for (int s = slot0; s < slot1; s += NS) {
       turn(GE_I(0), s);
-      if (s + 1 < ns) turn(GE_I(1), s + 1);
-      if constexpr (NS > 2) {
-        if (s + 2 < ns) turn(GE_I(2), s + 2);
-      }
+      turn(GE_I(1), s + 1);
+      if constexpr (NS > 2) turn(GE_I(2), s + 2);
+      if constexpr (NS > 3) turn(GE_I(3), s + 3);
+      if constexpr (NS > 4) turn(GE_I(4), s + 4);
     }
   }
 #undef GE_I
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));      // loads past the end, last fragment reads
   __syncthreads();                                     // every wave is done with the slots
+
+  // ---- a split contraction: every workgroup of the tile leaves its sums in the workspace, as the
+  // lanes hold them, and takes a ticket; the one that draws the last adds all up in split order
+  // (fixed, so equal calls give equal bits) and goes on to the epilogue.  Device-scope accesses
+  // and their order are those of ge_kernel_impl.h's reductions: the stores are performed before
+  // the ticket, the loads issued after it. ----
+  if constexpr (!T::PP) {
+    if (splits > 1) {                                  // uniform
+      typedef unsigned long long u64;
+      constexpr int BLOCKS = NB * T::FN * T::FM;
+      u64* const tile_part = (u64*)l.part + (int64_t)tile_id * splits * (BLOCKS * T::NT * 2);
+      u64* const mine = tile_part + (int64_t)split * (BLOCKS * T::NT * 2) + tid * 2;
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) {
+        u64 w[2];
+        __builtin_memcpy(w, &acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM], 16);
+        __hip_atomic_store(mine + b * (T::NT * 2), w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(mine + b * (T::NT * 2) + 1, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __builtin_amdgcn_s_waitcnt(kVmcnt0);
+      __syncthreads();
+      uint32_t* const flag = (uint32_t*)a0;
+      if (tid == 0) {
+        uint32_t* ctr = l.ctr + (uint32_t)tile_id * kFfnCtrStride;
+        const bool last = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)splits - 1u;
+        if (last) __hip_atomic_store(ctr, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *flag = last ? 1u : 0u;
+      }
+      __syncthreads();
+      if (*flag == 0u) return;                         // uniform
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] = f32x4_t{};
+      for (int q = 0; q < splits; ++q) {
+        const u64* from = tile_part + (int64_t)q * (BLOCKS * T::NT * 2) + tid * 2;
+        u64 w[BLOCKS][2];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+          w[b][0] = __hip_atomic_load(from + b * (T::NT * 2), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          w[b][1] = __hip_atomic_load(from + b * (T::NT * 2) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+          f32x4_t o;
+          __builtin_memcpy(&o, w[b], 16);
+          acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] += o;
+        }
+      }
+    }
+  }
 
   // ---- epilogue, per 32-row block of the wave's tile ----
   // Registers hold four consecutive columns of a row per lane and block; each value set goes to a
@@ -521,17 +598,21 @@ void ffn_product(FfnLaunch l) {
   }
 }
 
-using F256 = FTile<256, 256, 1, 8, 2>;      // 128 x 64 per wave
-using F256P = FTile<256, 128, 2, 8, 2>;     // 128 x 32 (x2: gate, up) per wave
-using F128 = FTile<128, 128, 1, 4, 3>;      // 64 x 64 per wave
-using F128P = FTile<128, 128, 2, 4, 2>;
-using F64 = FTile<64, 64, 1, 4, 3>;         // 32 x 32 per wave
+// The 128-row tiles run eight waves (two per SIMD, 64 x 32 each) with 96 KB of loads in flight, the
+// 64-row ones four waves and two or three workgroups per CU.  Measured per 64-deep slot with every CU
+// busy: 1.5 us (256), 0.45-0.6 us (128; with four waves 0.6-0.65), 0.21 us (64).
+using F256 = FTile<256, 256, 1, 8, 2, true>;      // 128 x 64 per wave
+using F256P = FTile<256, 128, 2, 8, 2, true>;     // 128 x 32 (x2: gate, up) per wave
+using F128 = FTile<128, 128, 1, 8, 4>;            // 64 x 32 per wave
+using F128P = FTile<128, 128, 2, 8, 3>;
+using F64 = FTile<64, 64, 1, 4, 4>;               // 32 x 32 per wave
 using F64P = FTile<64, 64, 2, 4, 3>;
 
 template <class T, int MODE, int ACT, bool AC, bool BC>
 hipError_t launch_product(const FfnLaunch& l, hipStream_t s) {
   if (l.tiles <= 0) return hipSuccess;
-  hipLaunchKernelGGL((ffn_product<T, MODE, ACT, AC, BC>), dim3((unsigned)l.tiles), dim3(T::NT), 0, s, l);
+  hipLaunchKernelGGL((ffn_product<T, MODE, ACT, AC, BC>), dim3((unsigned)(l.tiles * (T::PP ? 1 : l.splits))),
+                     dim3(T::NT), 0, s, l);
   return hipGetLastError();
 }
 

@@ -154,12 +154,38 @@ def test_tiles_give_equal_bits(layout):
 def test_many_tiles(M, d, h, layout):
     """Several rounds of the largest tile on every compute unit, each race a chance to show."""
     c = Case(M, d, h, layout=layout)
-    f, b = c.forward(), c.backward()
+    c.check_forward(c.forward(), "auto")
+    c.check_backward(c.backward(), "auto")
+    f, b = c.forward(tile=block.GE_FFN_TILE_256), c.backward(tile=block.GE_FFN_TILE_256)
     c.check_forward(f, "forward")
     c.check_backward(b, "backward")
     small = {**c.forward(tile=block.GE_FFN_TILE_64), **c.backward(tile=block.GE_FFN_TILE_64)}
     for k, v in {**f, **b}.items():
         assert torch.equal(v, small[k]), k
+
+
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("M,d,h", [(64, 264, 4104), (40, 2056, 264), (96, 4104, 520), (4100, 72, 136), (130, 1032, 3080),
+                                   (20, 520, 4104), (9, 4104, 136)])
+def test_split_contractions(M, d, h, layout):
+    """Long contractions over few tiles are split over workgroups; the sums meet in one order, so
+    that runs agree bit for bit, also when the workspace holds another call's remains."""
+    c = Case(M, d, h, layout=layout)
+    plan = c.plan()
+    first = {**c.forward(plan=plan), **c.backward(plan=plan)}
+    c.check_forward({k: first[k] for k in ("Y", "G", "U")}, plan.describe())
+    c.check_backward({k: first[k] for k in ("dX", "dWg", "dWu", "dWd")}, plan.describe())
+    for _ in range(5):
+        again = {**c.forward(plan=plan), **c.backward(plan=plan)}
+        for k in first:
+            assert torch.equal(first[k], again[k]), (k, plan.describe())
+
+
+def test_splits_are_chosen():
+    """The sizes above reach the split kernels of every product (one at least each)."""
+    seen = [Case(*s).plan().describe() for s in ((64, 264, 4104), (40, 2056, 264), (96, 4104, 520), (4100, 72, 136))]
+    for name in ("pair", "down", "grad", "dx", "dw"):
+        assert any(int(w.split("/")[1]) > 1 for line in seen for w in line.split() if w.startswith(name + "=")), (name, seen)
 
 
 def test_empty_sizes():
