@@ -39,18 +39,19 @@ constexpr int64_t kFewRows = 32;
 constexpr int kMaxSplits = 16;
 constexpr int kMaxSplitGroups = 768;
 
-// Tile and splits of one launch: the least estimated time.  A workgroup of a tile needs `slot` us
-// for 64 values of the contraction and `fixed` us around them; `per_cu` of them share a compute
-// unit's time beyond the first.  A split adds the partial sums' way through memory.  The figures
-// are measured (ge_ffn_impl.h); they need only rank the choices.
+// Tile and splits of one launch: the least estimated time in microseconds.  A tile costs `fixed` and
+// `slot` for every 64 values of the contraction, `crowd` instead where workgroups share a compute
+// unit or come in rounds; a split adds the partial sums' way through memory and back.  The figures
+// were measured over grids of 64 to 768 workgroups; they need only rank the choices.
 using Choice = ge_ffn_plan::Choice;
 Choice pick(int mode, int64_t M, int64_t N, int64_t K, int products, int32_t asked) {
   if (asked) return Choice{asked - 1, 1};
-  const bool pair = mode == ge::FFN_PAIR;
+  const bool pair = mode == ge::FFN_PAIR, dw = mode == ge::FFN_WGRAD;
   const int64_t slots = ceil_div(K, 64) * (mode == ge::FFN_DUAL ? 2 : 1);
-  struct Cost { double fixed, slot, crowd; };           // crowd: a slot with several workgroups per CU, each
-  const Cost cost[ge::FFN_TILES] = {{12.0, 1.4, 1.4}, {6.0, pair ? 1.0 : 0.5, pair ? 1.0 : 0.55},
-                                    {4.5, pair ? 0.45 : 0.26, pair ? 0.43 : 0.21}};
+  struct Cost { double fixed, slot, crowd; };
+  const Cost cost[ge::FFN_TILES] = {{7.0, 1.3, 1.4},
+                                    {3.0, pair ? 1.0 : 0.5, pair ? 1.0 : dw ? 0.65 : 0.57},
+                                    {1.5, pair ? 0.45 : 0.26, pair ? 0.43 : dw ? 0.27 : 0.21}};
   Choice best{ge::FFN_T64, 1};
   double least = 1e300;
   for (int t = 0; t < ge::FFN_TILES; ++t) {
@@ -59,8 +60,10 @@ Choice pick(int mode, int64_t M, int64_t N, int64_t K, int products, int32_t ask
     const double tiles = (double)ceil_div(M, ti.bm) * (double)ceil_div(N, bn) * products;
     for (int s = 1; s <= (t == ge::FFN_T256 ? 1 : kMaxSplits); s *= 2) {
       if (s > 1 && (slots < 4 * s || tiles * s > kMaxSplitGroups)) break;
-      const double rounds = std::ceil(tiles * s / 256.0), mine = (double)ceil_div(slots, s);
-      double us = cost[t].fixed + mine * (rounds > 1 ? rounds * cost[t].crowd : cost[t].slot);
+      // (workgroups of many rounds no longer end together)
+      const double ratio = tiles * s / 256.0, rounds = ratio < 4.0 ? std::ceil(ratio) : ratio;
+      const double mine = (double)ceil_div(slots, s);
+      double us = rounds > 1.0 ? rounds * (cost[t].fixed + mine * cost[t].crowd) : cost[t].fixed + mine * cost[t].slot;
       if (s > 1) us += 2.5 + tiles * s * ti.bm * bn * (pair ? 8.0 : 4.0) * 2 / 3e6;
       if (us < least) {
         least = us;

@@ -25,6 +25,7 @@ struct ge_qk_plan {
 
 namespace {
 
+constexpr int kMostTokens = 16;          // of one turn
 constexpr int64_t kMaxTokens = int64_t(1) << 40, kMaxHeads = int64_t(1) << 20, kMaxStride = int64_t(1) << 40;
 
 // Heads of tokens as rows of elements: the larger stride separates rows.  Exact for the layouts
@@ -50,8 +51,11 @@ bool wide(const ge_qk_desc_t& d, const void* const* ptrs, int n_ptrs, const int6
   if (d.head_dim % 8 || d.rot_dim % 8) return false;
   for (int i = 0; i < n_ptrs; ++i)
     if (!aligned(ptrs[i], 16)) return false;
-  for (int i = 0; i < n_strides; ++i)
-    if (strides[i] % 8) return false;
+  // offsets within a turn's tokens: 24-bit factors, 31-bit byte offsets
+  for (int i = 0; i < n_strides; i += 2) {
+    if (strides[i] % 8 || strides[i + 1] % 8 || strides[i] >= (1 << 24) || strides[i + 1] >= (1 << 24)) return false;
+    if (strides[i] * kMostTokens + strides[i + 1] * std::max(d.heads_q, d.heads_k) >= (int64_t(1) << 28)) return false;
+  }
   return true;
 }
 
@@ -204,11 +208,11 @@ ge_status_t ge_qk_create(const ge_qk_desc_t* d, ge_qk_handle_t* handle) {
   if (d->tokens * heads <= 1024 * groups) {
     // few heads in all: one head per group of lanes, so that every compute unit has work
     p->tokens_per_wg = 1;
-    p->head_splits = (int)std::max<int64_t>(1, ceil_div(heads, groups));
+    p->head_splits = (int)std::max<int64_t>(1, ceil_div(std::max(d->heads_q, d->heads_k), groups));
   } else {
     // a workgroup turns one angle per thread, then all heads of those tokens
     const int rot2 = std::max(d->rot_dim / 2, 1);
-    p->tokens_per_wg = std::min(std::max(ge::kQkThreads / rot2, 1), 16);
+    p->tokens_per_wg = std::min(std::max(ge::kQkThreads / rot2, 1), kMostTokens);
     p->head_splits = 1;
   }
   const int64_t turns = heads > 0 ? ceil_div(d->tokens, p->tokens_per_wg) * p->head_splits : 0;

@@ -5,11 +5,14 @@
 // that both values of every rotation pair are in one lane: interleaved pairs are eight
 // consecutive values, half pairs four consecutive values of each half.  So the rotation needs no
 // exchange between lanes, a lane reads and writes the same elements (in place is safe), and only
-// the norm's sums cross lanes.
+// the norm's sums cross lanes.  Fused multiply-adds are written out: the kernels for aligned and for
+// any layout give the same bits.
 //
 // The angle position * inv_freq and its reduction to a turn are computed in 64 bits (positions go
 // past 2^24 turns' worth of fp32), its cosine and sine in 32, once per token and pair: a
 // workgroup computes those of its tokens into LDS and all heads of the tokens read them there.
+#include <type_traits>
+
 #include "ge_block_internal.h"
 
 namespace ge {
@@ -54,41 +57,65 @@ __device__ __forceinline__ int offset_b(int slot, int j, int rot2, int d2) {
 }
 
 // WIDE: rot_dim / 2 and head_dim / 2 multiples of four and 16-byte aligned heads, so a lane's slots are
-// all turned or all not, and its values are two runs of four (or one of eight).
-template <class E, bool WIDE, bool HALF>
-__device__ __forceinline__ Pairs load(const E* head, int slot, int rot2, int d2) {
+// all turned or all not, and its values are two runs of four (or one of eight).  Raw: the bytes as
+// loaded, so that the next heads' loads can be on their way while one is computed.
+template <class E, bool WIDE>
+struct Raw {
   Pairs v;
+};
+template <>
+struct Raw<uint16_t, true> {
+  u32x4 v;
+};
+
+template <class E, bool WIDE, bool HALF>
+__device__ __forceinline__ void load(Raw<E, WIDE>& raw, const E* head, int slot, int rot2, int d2) {
   if constexpr (WIDE) {
-    if constexpr (HALF) {
-      // not turned: the pairing does not matter, take the runs as they come
-      const int oa = slot < rot2 ? slot : 2 * slot, ob = slot < rot2 ? slot + rot2 : 2 * slot + 4;
-      if constexpr (sizeof(E) == 2) {
+    // half pairs that are not turned: the pairing does not matter, take the runs as they come
+    const int oa = HALF && slot < rot2 ? slot : 2 * slot, ob = HALF && slot < rot2 ? slot + rot2 : 2 * slot + 4;
+    if constexpr (sizeof(E) == 2) {
+      if constexpr (HALF) {
         const u32x2 x = *(const u32x2*)(head + oa), y = *(const u32x2*)(head + ob);
-        v.a[0] = lo(x[0]); v.a[1] = hi(x[0]); v.a[2] = lo(x[1]); v.a[3] = hi(x[1]);
-        v.b[0] = lo(y[0]); v.b[1] = hi(y[0]); v.b[2] = lo(y[1]); v.b[3] = hi(y[1]);
+        raw.v = u32x4{x[0], x[1], y[0], y[1]};
       } else {
-        const f32x4 x = *(const f32x4*)(head + oa), y = *(const f32x4*)(head + ob);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { v.a[j] = x[j]; v.b[j] = y[j]; }
+        raw.v = *(const u32x4*)(head + oa);
       }
-    } else if constexpr (sizeof(E) == 2) {
-      const u32x4 x = *(const u32x4*)(head + 2 * slot);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { v.a[j] = lo(x[j]); v.b[j] = hi(x[j]); }
     } else {
-      const f32x4 x = *(const f32x4*)(head + 2 * slot), y = *(const f32x4*)(head + 2 * slot + 4);
-      v.a[0] = x[0]; v.b[0] = x[1]; v.a[1] = x[2]; v.b[1] = x[3];
-      v.a[2] = y[0]; v.b[2] = y[1]; v.a[3] = y[2]; v.b[3] = y[3];
+      const f32x4 x = *(const f32x4*)(head + oa), y = *(const f32x4*)(head + ob);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { raw.v.a[j] = x[j]; raw.v.b[j] = y[j]; }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool ok = slot + j < d2;
-      v.a[j] = ok ? one(head + offset_a<HALF>(slot, j, rot2, d2)) : 0.0f;
-      v.b[j] = ok ? one(head + offset_b<HALF>(slot, j, rot2, d2)) : 0.0f;
+      raw.v.a[j] = ok ? one(head + offset_a<HALF>(slot, j, rot2, d2)) : 0.0f;
+      raw.v.b[j] = ok ? one(head + offset_b<HALF>(slot, j, rot2, d2)) : 0.0f;
     }
   }
-  return v;
+}
+// Two runs of four to pairs: half pairs as they are, interleaved pairs neighbour by neighbour.
+template <class E, bool WIDE, bool HALF>
+__device__ __forceinline__ Pairs pairs_of(const Raw<E, WIDE>& raw) {
+  if constexpr (!WIDE) {
+    return raw.v;
+  } else {
+    float x[8];
+    if constexpr (sizeof(E) == 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { x[2 * j] = lo(raw.v[j]); x[2 * j + 1] = hi(raw.v[j]); }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { x[j] = raw.v.a[j]; x[4 + j] = raw.v.b[j]; }
+    }
+    Pairs v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v.a[j] = HALF ? x[j] : x[2 * j];
+      v.b[j] = HALF ? x[4 + j] : x[2 * j + 1];
+    }
+    return v;
+  }
 }
 
 template <class E, bool WIDE, bool HALF>
@@ -120,15 +147,38 @@ __device__ __forceinline__ void store(E* head, int slot, int rot2, int d2, const
   }
 }
 
+// Sum over the lanes of a group, the same bits in each: exchanges within 16 lanes are DPP operands
+// of the adds (after the first two steps quads agree, so mirrored halves stand for the further ones).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float group_sum(float v, int G) {
+  if (G >= 2) v = dpp_add<0xB1>(v);       // quad: lanes 1 0 3 2
+  if (G >= 4) v = dpp_add<0x4E>(v);       // quad: lanes 2 3 0 1
+  if (G >= 8) v = dpp_add<0x141>(v);      // mirrored in 8
+  if (G >= 16) v = dpp_add<0x140>(v);     // mirrored in 16
+  if (G >= 32) v += __shfl_xor(v, 16);
+  if (G >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Element offset of a head within a turn's tokens.  WIDE: 24-bit factors, 31-bit products (checked
+// on the host), so the addresses take two full-rate multiplies.
+template <bool WIDE>
+__device__ __forceinline__ auto head_at(int t, int h, int64_t st, int64_t sh) {
+  if constexpr (WIDE) return (uint32_t)(__umul24((uint32_t)t, (uint32_t)st) + __umul24((uint32_t)h, (uint32_t)sh));
+  else return (int64_t)t * st + (int64_t)h * sh;
+}
+
 template <class E, bool WIDE, bool HALF, bool NORM, bool BWD>
 __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
-  __shared__ float2 turn[kQkMaxAngles];
+  __shared__ __attribute__((aligned(16))) float2 turn[kQkMaxAngles];
   __shared__ float gsum[BWD && NORM ? 2 * 8 * kQkThreads : 1];
   const int tid = threadIdx.x, G = p.group;
   const int gl = tid & (G - 1), ng = kQkThreads / G, grp = tid / G;
   const int slot = 4 * gl, rot2 = p.rot_dim / 2, d2 = p.head_dim / 2;
   const bool live = slot < d2;
-  const int heads = p.heads[0] + p.heads[1];
   const float inv_d = 1.0f / (float)p.head_dim;
 
   Pairs gain[2];
@@ -148,120 +198,138 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) dgain[w].a[j] = dgain[w].b[j] = 0.0f;
 
+  struct Item {
+    Raw<E, WIDE> x, d;
+  };
   const int tw = p.tokens_per_wg, hs = p.head_splits;
   const int64_t turns = (p.tokens + tw - 1) / tw * hs;
   for (int64_t it = blockIdx.x; it < turns; it += gridDim.x) {
     const int64_t t0 = it / hs * tw;
     const int part = (int)(it % hs);
     const int nt = (int)(p.tokens - t0 < tw ? p.tokens - t0 : tw);
-    if (rot2 > 0) {
-      __syncthreads();                                 // the last turn's readers are done
-      for (int i = tid; i < nt * rot2; i += kQkThreads) {
-        const int t = i / rot2, f = i - t * rot2;
-        const double pos = p.pos64 ? (double)((const int64_t*)p.positions)[t0 + t] : (double)((const int32_t*)p.positions)[t0 + t];
-        double turns_of = pos * (double)p.inv_freq[f] * 0.15915494309189533577;     // angle / 2 pi
-        turns_of -= __builtin_rint(turns_of);
-        float s, c;
-        sincospif(2.0f * (float)turns_of, &s, &c);
-        turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
-      }
-      __syncthreads();
-    }
-    // (token, head) items of this turn, one per group and step; a split takes every hs-th run of heads
-    const int h_lo = (int)((int64_t)heads * part / hs), nh = (int)((int64_t)heads * (part + 1) / hs) - h_lo;
-    if (nh <= 0) continue;                             // uniform
-    const int step_t = ng / nh, step_h = ng - step_t * nh;
-    int t = grp / nh, h = grp - t * nh;
-    while (t < nt) {
-      const int hh = h_lo + h, w = hh >= p.heads[0] ? 1 : 0, hw = hh - (w ? p.heads[0] : 0);
-      const int64_t tok = t0 + t;
-      Pairs x, d, o;
-      if constexpr (!BWD || NORM) {
-        const E* px = (const E*)p.x[w] + tok * p.xt[w] + hw * p.xh[w];
-        if (live) x = load<E, WIDE, HALF>(px, slot, rot2, d2);
-      }
-      if constexpr (BWD) {
-        const E* pd = (const E*)p.dy[w] + tok * p.dt[w] + hw * p.dh[w];
-        if (live) d = load<E, WIDE, HALF>(pd, slot, rot2, d2);
-      }
-      float cs[4], sn[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cs[j] = 1.0f;
-        sn[j] = 0.0f;
-        if (slot + j < rot2) {
-          const float2 a = turn[t * rot2 + slot + j];
-          cs[j] = a.x;
-          sn[j] = a.y;
+    // All heads of the queries, then those of the keys: which of the two is uniform.  One item (a
+    // head of a token) per group and step; the next one is loaded before this one is computed.
+    auto side = [&](auto w_c, bool angles) {
+      constexpr int w = decltype(w_c)::value;
+      const int h_lo = (int)((int64_t)p.heads[w] * part / hs), nh = (int)((int64_t)p.heads[w] * (part + 1) / hs) - h_lo;
+      const E* const px = (const E*)p.x[w] + t0 * p.xt[w] + h_lo * p.xh[w];
+      const E* const pd = (const E*)p.dy[w] + t0 * p.dt[w] + h_lo * p.dh[w];
+      E* const py = (E*)p.y[w] + t0 * p.yt[w] + h_lo * p.yh[w];
+      const int steps = nh > 0 ? (nt * nh + ng - 1) / ng : 0;          // uniform
+      const int step_t = nh > 0 ? ng / nh : 0, step_h = ng - step_t * nh;
+      int t = nh > 0 ? grp / nh : nt, h = nh > 0 ? grp - t * nh : 0;
+      auto fetch = [&](Item& i) {
+        if (t < nt && live) {
+          if constexpr (!BWD || NORM) load<E, WIDE, HALF>(i.x, px + head_at<WIDE>(t, h, p.xt[w], p.xh[w]), slot, rot2, d2);
+          if constexpr (BWD) load<E, WIDE, HALF>(i.d, pd + head_at<WIDE>(t, h, p.dt[w], p.dh[w]), slot, rot2, d2);
         }
-      }
-      if (!live) {
+      };
+      auto work = [&](const Item& i, int t, int h) {
+        Pairs x, d, o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) x.a[j] = x.b[j] = d.a[j] = d.b[j] = 0.0f;
-      }
-      if constexpr (!BWD) {
-        if constexpr (NORM) {
-          float ss = 0.0f;
+        if (live) {
+          if constexpr (!BWD || NORM) x = pairs_of<E, WIDE, HALF>(i.x);
+          if constexpr (BWD) d = pairs_of<E, WIDE, HALF>(i.d);
+        }
+        float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (WIDE) {
+          if (slot < rot2) {
+            const f32x4 u = *(const f32x4*)(turn + t * rot2 + slot), v = *(const f32x4*)(turn + t * rot2 + slot + 2);
+            cs[0] = u[0]; sn[0] = u[1]; cs[1] = u[2]; sn[1] = u[3];
+            cs[2] = v[0]; sn[2] = v[1]; cs[3] = v[2]; sn[3] = v[3];
+          }
+        } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ss += x.a[j] * x.a[j] + x.b[j] * x.b[j];
-          for (int m = 1; m < G; m <<= 1) ss += __shfl_xor(ss, m);
-          const float r = 1.0f / sqrtf(ss * inv_d + p.eps);
+          for (int j = 0; j < 4; ++j)
+            if (slot + j < rot2) {
+              const float2 a = turn[t * rot2 + slot + j];
+              cs[j] = a.x;
+              sn[j] = a.y;
+            }
+        }
+        if constexpr (!BWD) {
+          if constexpr (NORM) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = fmaf(x.a[j], x.a[j], fmaf(x.b[j], x.b[j], ss));
+            const float r = __builtin_amdgcn_rsqf(fmaf(group_sum(ss, G), inv_d, p.eps));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x.a[j] = x.a[j] * r * gain[w].a[j];
+              x.b[j] = x.b[j] * r * gain[w].b[j];
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            x.a[j] = x.a[j] * r * (w ? gain[1].a[j] : gain[0].a[j]);
-            x.b[j] = x.b[j] * r * (w ? gain[1].b[j] : gain[0].b[j]);
+            o.a[j] = fmaf(x.a[j], cs[j], -(x.b[j] * sn[j]));
+            o.b[j] = fmaf(x.b[j], cs[j], x.a[j] * sn[j]);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o.a[j] = x.a[j] * cs[j] - x.b[j] * sn[j];
-          o.b[j] = x.b[j] * cs[j] + x.a[j] * sn[j];
-        }
-      } else {
-        // the rotation's transpose, then the norm's derivative: with n = x r and e = dy * gain,
-        // dx = r (e - n mean(e n)) and dgain += dy n
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o.a[j] = d.a[j] * cs[j] + d.b[j] * sn[j];
-          o.b[j] = d.b[j] * cs[j] - d.a[j] * sn[j];
-        }
-        if constexpr (NORM) {
-          float ss = 0.0f, ex = 0.0f;
-          Pairs e;
+        } else {
+          // the rotation's transpose, then the norm's derivative: with n = x r and e = dy * gain,
+          // dx = r (e - n mean(e n)) and dgain += dy n
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            e.a[j] = o.a[j] * (w ? gain[1].a[j] : gain[0].a[j]);
-            e.b[j] = o.b[j] * (w ? gain[1].b[j] : gain[0].b[j]);
-            ss += x.a[j] * x.a[j] + x.b[j] * x.b[j];
-            ex += e.a[j] * x.a[j] + e.b[j] * x.b[j];
+            o.a[j] = fmaf(d.a[j], cs[j], d.b[j] * sn[j]);
+            o.b[j] = fmaf(d.b[j], cs[j], -(d.a[j] * sn[j]));
           }
-          for (int m = 1; m < G; m <<= 1) {
-            ss += __shfl_xor(ss, m);
-            ex += __shfl_xor(ex, m);
-          }
-          const float r = 1.0f / sqrtf(ss * inv_d + p.eps);
-          const float mean = ex * r * inv_d;
+          if constexpr (NORM) {
+            float ss = 0.0f, ex = 0.0f;
+            Pairs e;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float na = x.a[j] * r, nb = x.b[j] * r;
-            const float ga = o.a[j] * na, gb = o.b[j] * nb;
-            dgain[0].a[j] += w ? 0.0f : ga;
-            dgain[0].b[j] += w ? 0.0f : gb;
-            dgain[1].a[j] += w ? ga : 0.0f;
-            dgain[1].b[j] += w ? gb : 0.0f;
-            o.a[j] = r * (e.a[j] - na * mean);
-            o.b[j] = r * (e.b[j] - nb * mean);
+            for (int j = 0; j < 4; ++j) {
+              e.a[j] = o.a[j] * gain[w].a[j];
+              e.b[j] = o.b[j] * gain[w].b[j];
+              ss = fmaf(x.a[j], x.a[j], fmaf(x.b[j], x.b[j], ss));
+              ex = fmaf(e.a[j], x.a[j], fmaf(e.b[j], x.b[j], ex));
+            }
+            ss = group_sum(ss, G);
+            ex = group_sum(ex, G);
+            const float r = __builtin_amdgcn_rsqf(fmaf(ss, inv_d, p.eps));
+            const float mean = ex * r * inv_d;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float na = x.a[j] * r, nb = x.b[j] * r;
+              dgain[w].a[j] = fmaf(o.a[j], na, dgain[w].a[j]);
+              dgain[w].b[j] = fmaf(o.b[j], nb, dgain[w].b[j]);
+              o.a[j] = r * fmaf(-na, mean, e.a[j]);
+              o.b[j] = r * fmaf(-nb, mean, e.b[j]);
+            }
           }
         }
+        if (live) store<E, WIDE, HALF>(py + head_at<WIDE>(t, h, p.yt[w], p.yh[w]), slot, rot2, d2, o);
+      };
+      Item now, next;
+      fetch(now);
+      if (angles && rot2 > 0) {                        // uniform
+        __syncthreads();                               // the last turn's readers are done
+        for (int i = tid; i < nt * rot2; i += kQkThreads) {
+          const int q = i / rot2, f = i - q * rot2;
+          const double pos =
+              p.pos64 ? (double)((const int64_t*)p.positions)[t0 + q] : (double)((const int32_t*)p.positions)[t0 + q];
+          double turns_of = pos * (double)p.inv_freq[f] * 0.15915494309189533577;     // angle / 2 pi
+          turns_of -= __builtin_rint(turns_of);
+          float s, c;
+          sincospif(2.0f * (float)turns_of, &s, &c);
+          turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+        }
+        __syncthreads();
       }
-      if (live) store<E, WIDE, HALF>((E*)p.y[w] + tok * p.yt[w] + hw * p.yh[w], slot, rot2, d2, o);
-      t += step_t;
-      h += step_h;
-      if (h >= nh) {
-        h -= nh;
-        ++t;
+      for (int k = 0; k < steps; ++k) {                // uniform
+        const int t_now = t, h_now = h;
+        t += step_t;
+        h += step_h;
+        if (h >= nh) {
+          h -= nh;
+          ++t;
+        }
+        fetch(next);
+        if (t_now < nt) work(now, t_now, h_now);       // the same for a whole group
+        now = next;
       }
-    }
+    };
+    side(std::integral_constant<int, 0>{}, true);
+    side(std::integral_constant<int, 1>{}, false);
   }
 
   if constexpr (BWD && NORM) {
