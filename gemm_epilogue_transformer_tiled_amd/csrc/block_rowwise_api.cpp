@@ -210,14 +210,18 @@ ge_status_t ge_qk_create(const ge_qk_desc_t* d, ge_qk_handle_t* handle) {
     p->tokens_per_wg = 1;
     p->head_splits = (int)std::max<int64_t>(1, ceil_div(std::max(d->heads_q, d->heads_k), groups));
   } else {
-    // a workgroup turns one angle per thread, then all heads of those tokens
+    // a workgroup turns about one angle per thread, then all heads of those tokens; fewer tokens
+    // where that would leave less than four workgroups for a compute unit
     const int rot2 = std::max(d->rot_dim / 2, 1);
-    p->tokens_per_wg = std::min(std::max(ge::kQkThreads / rot2, 1), kMostTokens);
+    const int64_t most = std::min<int64_t>(std::max(ge::kQkThreads / rot2, 1), kMostTokens);
+    p->tokens_per_wg = (int)std::min(most, std::max<int64_t>(1, d->tokens / 1024));
     p->head_splits = 1;
   }
   const int64_t turns = heads > 0 ? ceil_div(d->tokens, p->tokens_per_wg) * p->head_splits : 0;
   p->grid_forward = (int)std::min<int64_t>(turns, 1 << 20);
-  p->grid_backward = (int)std::min<int64_t>(turns, d->norm ? ge::kQkMaxBackwardGrid : 1 << 20);
+  // with the norm every workgroup leaves partial sums: at least four turns each, or 512 workgroups
+  p->grid_backward = (int)std::min<int64_t>(
+      turns, d->norm ? std::min<int64_t>(ge::kQkMaxBackwardGrid, std::max<int64_t>(512, turns / 4)) : 1 << 20);
   *handle = p;
   return GE_OK;
 }
@@ -260,6 +264,7 @@ ge_status_t ge_qk_backward(ge_qk_handle_t h, const ge_qk_args_t* a, void* stream
 struct ge_clip_plan {
   ge_clip_tensor_t* t;
   int32_t n, live;            // tensors, and those that are not empty
+  int policy;                 // ge::ClipPolicy
   int device;
 };
 
@@ -285,11 +290,12 @@ ge_status_t ge_clip_create(const ge_clip_tensor_t* tensors, int32_t n, ge_clip_h
     if (tensors[i].numel < 0 || (tensors[i].dtype != GE_DT_BF16 && tensors[i].dtype != GE_DT_FP32 &&
                                  tensors[i].dtype != GE_DT_FP8_E4M3))
       return GE_ERR_INVALID_ARG;
-  int64_t all = 0, live = 0;
+  int64_t all = 0, live = 0, bytes = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (tensors[i].dtype == GE_DT_FP8_E4M3) return GE_ERR_UNSUPPORTED;
     if (tensors[i].numel >= (int64_t(1) << 45) || (all += tensors[i].numel) >= (int64_t(1) << 45)) return GE_ERR_UNSUPPORTED;
     live += tensors[i].numel > 0;
+    bytes += tensors[i].numel * (tensors[i].dtype == GE_DT_BF16 ? 2 : 4);
   }
   // each launch and, in the workspace, each of its workgroups has a partial sum
   if (live > (int64_t)ge::kClipTensors * 256) return GE_ERR_UNSUPPORTED;
@@ -305,6 +311,7 @@ ge_status_t ge_clip_create(const ge_clip_tensor_t* tensors, int32_t n, ge_clip_h
   std::copy(tensors, tensors + n, p->t);
   p->n = n;
   p->live = (int32_t)live;
+  p->policy = ge::clip_policy(bytes);
   p->device = device;
   *handle = p;
   return GE_OK;
@@ -391,10 +398,10 @@ ge_status_t ge_clip_run(ge_clip_handle_t h, const ge_clip_args_t* a, void* strea
       const int grid = (int)std::min<int64_t>(chunks, pass == 0 ? most : ge::kClipPartials);
       hipError_t e;
       if (pass == 0) {
-        e = ge::launch_clip_norm(t, grid, part + nparts, s);
+        e = ge::launch_clip_norm(t, grid, h->policy, part + nparts, s);
         nparts += grid;
       } else {
-        e = ge::launch_clip_scale(t, grid, part, nparts, a->max_norm, a->eps, l == 0 ? a->norm : nullptr, s);
+        e = ge::launch_clip_scale(t, grid, h->policy, part, nparts, a->max_norm, a->eps, l == 0 ? a->norm : nullptr, s);
       }
       if (e != hipSuccess) return GE_ERR_HIP;
     }

@@ -85,7 +85,7 @@ hipError_t launch_qk(const QkKind& kind, const QkParams& p, hipStream_t s);
 hipError_t launch_qk_gains(const float* part, int rows, int head_dim, float* dgain_q, float* dgain_k, hipStream_t s);
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxAngles = 1024;      // angles of one turn kept in LDS (8 KB)
-constexpr int kQkMaxBackwardGrid = 768;
+constexpr int kQkMaxBackwardGrid = 1024;
 
 // ---- gradient norm and clipping ----
 constexpr int kClipTensors = 128;       // tensors of one launch (its table travels as the argument)
@@ -99,10 +99,14 @@ struct ClipTable {
   uint32_t fp32[kClipTensors / 32];     // bit t: tensor t is fp32
   int32_t n;
 };
-hipError_t launch_clip_norm(const ClipTable& t, int grid, double* part, hipStream_t s);
+enum ClipPolicy : int { kClipCached = 0, kClipStoreThrough = 1, kClipStream = 2 };   // ge_clip.hip
+inline int clip_policy(int64_t bytes) {
+  return bytes > (int64_t(512) << 20) ? kClipStream : bytes > (int64_t(64) << 20) ? kClipStoreThrough : kClipCached;
+}
+hipError_t launch_clip_norm(const ClipTable& t, int grid, int policy, double* part, hipStream_t s);
 // nparts partial sums -> *norm (if any)
 hipError_t launch_clip_finish(const double* part, int nparts, float* norm, hipStream_t s);
-hipError_t launch_clip_scale(const ClipTable& t, int grid, const double* part, int nparts, float max_norm, float eps,
-                             float* norm, hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable& t, int grid, int policy, const double* part, int nparts, float max_norm,
+                             float eps, float* norm, hipStream_t s);
 
 }  // namespace ge

@@ -16,8 +16,25 @@ namespace {
 
 // 16-byte accesses at the elements' alignment: gradients packed one after another start anywhere
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
+typedef u32x4 Any16 __attribute__((aligned(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Cache policy by the gradients' bytes (kClip*, ge_block_internal.h).  The clipped values are not
+// read here again: past 64 MB they are stored "nt" (180 MB of gradients: 94 -> 85 us a call).  Past
+// 512 MB the second read finds almost nothing in the 256 MB memory-side cache, and every access
+// goes "nt" (2.2 GB: 1,205 -> 1,123 us; the norm alone then reads 6.9 TB/s instead of 6.1); below, that would
+// lose what the cache keeps (180 MB: 85 -> 98 us).
+template <int POLICY>
+__device__ __forceinline__ u32x4 fetch(const void* p) {
+  const Any16* q = (const Any16*)p;
+  if constexpr (POLICY >= kClipStream) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <int POLICY>
+__device__ __forceinline__ void put(void* p, u32x4 v) {
+  Any16* q = (Any16*)p;
+  if constexpr (POLICY >= kClipStoreThrough) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -46,6 +63,7 @@ __device__ __forceinline__ double block_sum(double s, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+template <int POLICY>
 __global__ __launch_bounds__(kThreads) void clip_norm(ClipTable t, double* part) {
   __shared__ double lds[4];
   double s = 0.0;
@@ -57,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void clip_norm(ClipTable t, double* part)
     if ((t.fp32[k >> 5] >> (k & 31)) & 1u) {
       const float* x = (const float*)t.in[k] + at;
       for (int i = 4 * threadIdx.x; i + 4 <= n; i += 4 * kThreads) {
-        const u32x4 w = ((const Any16*)(x + i))->v;
+        const u32x4 w = fetch<POLICY>(x + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) { const double v = (double)__uint_as_float(w[j]); s += v * v; }
       }
@@ -66,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void clip_norm(ClipTable t, double* part)
     } else {
       const uint16_t* x = (const uint16_t*)t.in[k] + at;
       for (int i = 8 * threadIdx.x; i + 8 <= n; i += 8 * kThreads) {
-        const u32x4 w = ((const Any16*)(x + i))->v;
+        const u32x4 w = fetch<POLICY>(x + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const double a = (double)lo(w[j]), b = (double)hi(w[j]);
@@ -95,6 +113,7 @@ __global__ __launch_bounds__(kThreads) void clip_finish(const double* part, int 
   if (threadIdx.x == 0) *norm = (float)sqrt(s);
 }
 
+template <int POLICY>
 __global__ __launch_bounds__(kThreads) void clip_scale(ClipTable t, const double* part, int nparts, float max_norm, float eps,
                                                        float* norm) {
   __shared__ double lds[4];
@@ -119,10 +138,10 @@ __global__ __launch_bounds__(kThreads) void clip_scale(ClipTable t, const double
       const float* x = (const float*)t.in[k] + at;
       float* y = (float*)t.out[k] + at;
       for (int i = 4 * threadIdx.x; i + 4 <= n; i += 4 * kThreads) {
-        u32x4 w = ((const Any16*)(x + i))->v;
+        u32x4 w = fetch<POLICY>(x + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(scaled(__uint_as_float(w[j])));
-        ((Any16*)(y + i))->v = w;
+        put<POLICY>(y + i, w);
       }
       const int i = (n & ~3) + (int)threadIdx.x;
       if (i < n) y[i] = scaled(x[i]);
@@ -130,10 +149,10 @@ __global__ __launch_bounds__(kThreads) void clip_scale(ClipTable t, const double
       const uint16_t* x = (const uint16_t*)t.in[k] + at;
       uint16_t* y = (uint16_t*)t.out[k] + at;
       for (int i = 8 * threadIdx.x; i + 8 <= n; i += 8 * kThreads) {
-        u32x4 w = ((const Any16*)(x + i))->v;
+        u32x4 w = fetch<POLICY>(x + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = pack2(scaled(lo(w[j])), scaled(hi(w[j])));
-        ((Any16*)(y + i))->v = w;
+        put<POLICY>(y + i, w);
       }
       const int i = (n & ~7) + (int)threadIdx.x;
       if (i < n) y[i] = (uint16_t)(pack2(scaled(lo(x[i])), 0.0f) & 0xFFFFu);
@@ -143,17 +162,23 @@ __global__ __launch_bounds__(kThreads) void clip_scale(ClipTable t, const double
 
 }  // namespace
 
-hipError_t launch_clip_norm(const ClipTable& t, int grid, double* part, hipStream_t s) {
-  hipLaunchKernelGGL(clip_norm, dim3((unsigned)grid), dim3(kThreads), 0, s, t, part);
+hipError_t launch_clip_norm(const ClipTable& t, int grid, int policy, double* part, hipStream_t s) {
+  if (policy >= kClipStream) hipLaunchKernelGGL(clip_norm<kClipStream>, dim3((unsigned)grid), dim3(kThreads), 0, s, t, part);
+  else hipLaunchKernelGGL(clip_norm<kClipCached>, dim3((unsigned)grid), dim3(kThreads), 0, s, t, part);
   return hipGetLastError();
 }
 hipError_t launch_clip_finish(const double* part, int nparts, float* norm, hipStream_t s) {
   hipLaunchKernelGGL(clip_finish, dim3(1), dim3(kThreads), 0, s, part, nparts, norm);
   return hipGetLastError();
 }
-hipError_t launch_clip_scale(const ClipTable& t, int grid, const double* part, int nparts, float max_norm, float eps,
-                             float* norm, hipStream_t s) {
-  hipLaunchKernelGGL(clip_scale, dim3((unsigned)grid), dim3(kThreads), 0, s, t, part, nparts, max_norm, eps, norm);
+hipError_t launch_clip_scale(const ClipTable& t, int grid, int policy, const double* part, int nparts, float max_norm,
+                             float eps, float* norm, hipStream_t s) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, t, part, nparts, max_norm, eps, norm);
+  };
+  if (policy == kClipCached) go(clip_scale<kClipCached>);
+  else if (policy == kClipStoreThrough) go(clip_scale<kClipStoreThrough>);
+  else go(clip_scale<kClipStream>);
   return hipGetLastError();
 }
 

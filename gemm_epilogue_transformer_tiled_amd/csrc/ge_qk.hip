@@ -352,19 +352,28 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
   }
 }
 
-// Sums the workgroups' partial gain gradients, 16 columns a workgroup, 16 threads a column, in a
+// Sums the workgroups' partial gain gradients, 16 columns a workgroup, 64 threads a column, in a
 // fixed order and in 64 bits.
-__global__ __launch_bounds__(256) void qk_gains(const float* part, int rows, int head_dim, float* dq, float* dk) {
-  __shared__ double sums[16][17];
-  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+__global__ __launch_bounds__(1024) void qk_gains(const float* part, int rows, int head_dim, float* dq, float* dk) {
+  __shared__ double sums[64][17];
+  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4, col = blockIdx.x * 16 + c, cols = 2 * head_dim;
   double s = 0.0;
-  if (col < 2 * head_dim)
-    for (int r = r0; r < rows; r += 16) s += (double)part[(int64_t)r * 2 * head_dim + col];
+  if (col < cols) {
+    int r = r0;
+    for (; r + 192 < rows; r += 256) {                 // four loads on their way
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(int64_t)(r + 64 * u) * cols + col];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s += (double)v[u];
+    }
+    for (; r < rows; r += 64) s += (double)part[(int64_t)r * cols + col];
+  }
   sums[r0][c] = s;
   __syncthreads();
-  if (r0 == 0 && col < 2 * head_dim) {
+  if (r0 == 0 && col < cols) {
     double all = 0.0;
-    for (int r = 0; r < 16; ++r) all += sums[r][c];
+    for (int r = 0; r < 64; ++r) all += sums[r][c];
     float* out = col < head_dim ? dq : dk;
     if (out) out[col < head_dim ? col : col - head_dim] = (float)all;
   }
@@ -393,7 +402,7 @@ hipError_t launch_qk(const QkKind& k, const QkParams& p, hipStream_t s) {
 }
 
 hipError_t launch_qk_gains(const float* part, int rows, int head_dim, float* dq, float* dk, hipStream_t s) {
-  hipLaunchKernelGGL(qk_gains, dim3((unsigned)((2 * head_dim + 15) / 16)), dim3(256), 0, s, part, rows, head_dim, dq, dk);
+  hipLaunchKernelGGL(qk_gains, dim3((unsigned)((2 * head_dim + 15) / 16)), dim3(1024), 0, s, part, rows, head_dim, dq, dk);
   return hipGetLastError();
 }
 
