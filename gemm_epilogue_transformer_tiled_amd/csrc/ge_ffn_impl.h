@@ -60,15 +60,27 @@ __device__ __forceinline__ uint32_t swz_col(uint32_t k) {
   return swz_b<CHUNKS>(k) ^ ((k >> 3) & 1u);
 }
 
-// activate_grad with the argument held where the derivative no longer changes in fp32, so that
-// squares of huge finite values do not turn 0 * inf into NaN (NaN arguments stay NaN).
+// act(z) and act'(z) from one exponential and one reciprocal.  The GELU's cubic is taken where it
+// still changes the sigmoid in fp32, so that squares of huge finite values do not turn 0 * inf into
+// NaN (NaN arguments stay NaN).
 template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-  if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
-    constexpr float L = 200.0f;
-    z = z > L ? L : (z < -L ? -L : z);
+__device__ __forceinline__ void act_and_slope(float z, float& a, float& s) {
+  if constexpr (ACT == ACT_RELU) {
+    a = fmaxf(z, 0.0f);
+    s = z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float c = z > 200.0f ? 200.0f : (z < -200.0f ? -200.0f : z), q = kGeluCubic * c * c;
+    const float g = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(kGeluC * c * (1.0f + q)));
+    a = z * g;
+    s = g + 2.0f * 0.7978845608028654f * c * g * (1.0f - g) * (1.0f + 3.0f * q);
+  } else if constexpr (ACT == ACT_SILU) {
+    const float g = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+    a = z * g;
+    s = g * (1.0f + z * (1.0f - g));
+  } else {
+    a = z;
+    s = 1.0f;
   }
-  return activate_grad<ACT>(z);
 }
 
 template <class T, int MODE, int ACT, bool AC, bool BC>
@@ -207,31 +219,35 @@ void ffn_product(FfnLaunch l) {
       b_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * ldb2 + (r_x ^ (u & 3u)) * 16u;
     }
   }
-  // Row operands: chunks past K get the out-of-range offset.  The chunk index is recomputed per
-  // fill (its input is opaque): kept in registers across the loop it spills the 256-row tiles.
+  // Row operands whose K is not a multiple of a slot: chunks past K get the out-of-range offset.
+  // The chunk index is recomputed per fill (its input is opaque): kept in registers across the loop it
+  // spills the 256-row tiles.  With K a multiple of 64 (WHOLE) a slot is inside K or its extent is
+  // empty: the loop without the masks' vector instructions is 10-20 % faster on two row operands.
   auto chunk_base = [&]() {
     uint32_t x = r_x;
     asm volatile("" : "+v"(x));
     return x;
   };
-  auto issue_a = [&](unsigned char* slot) {
-    const uint32_t x = AC ? 0u : chunk_base();
+  auto issue_a = [&](auto whole, unsigned char* slot) {
+    constexpr bool MASK = !AC && !decltype(whole)::value;
+    const uint32_t x = MASK ? chunk_base() : 0u;
 #pragma unroll
     for (int t = 0; t < T::LA; ++t) {
       const uint32_t u = (uint32_t)(wave * T::LA + t);
       uint32_t off = a_voff[t];
-      if constexpr (!AC) off = (int)((x ^ (u & 3u)) * 8u) < a_lim ? off : kOOB;
+      if constexpr (MASK) off = (int)((x ^ (u & 3u)) * 8u) < a_lim ? off : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (__attribute__((address_space(3))) void*)(slot + u * 1024), 16, off,
                                                0, 0, 0);
     }
   };
-  auto issue_b = [&](unsigned char* dst) {
-    const uint32_t x = BC ? 0u : chunk_base();
+  auto issue_b = [&](auto whole, unsigned char* dst) {
+    constexpr bool MASK = !BC && !decltype(whole)::value;
+    const uint32_t x = MASK ? chunk_base() : 0u;
 #pragma unroll
     for (int t = 0; t < LBF; ++t) {
       const uint32_t g = (uint32_t)(wave * LBF + t), u = g % (uint32_t)B_UNITS;   // wave-uniform
       uint32_t off = b_voff[t];
-      if constexpr (!BC) off = (int)((x ^ (u & 3u)) * 8u) < b_lim ? off : kOOB;
+      if constexpr (MASK) off = (int)((x ^ (u & 3u)) * 8u) < b_lim ? off : kOOB;
       if (PAIR && g >= (uint32_t)B_UNITS)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(brs2, (__attribute__((address_space(3))) void*)(dst + g * 1024), 16, off,
                                                  0, 0, 0);
@@ -325,6 +341,7 @@ void ffn_product(FfnLaunch l) {
     asm volatile("" ::: "memory");
   };
 
+  auto run = [&](auto whole) {
   if constexpr (T::PP) {
     // ---- two wave groups, one phase apart (ge_kernel_impl.h describes the phases) ----
     // Even steps j load the A slot of steps j+2, j+3; with a column B odd steps load its stages
@@ -332,13 +349,13 @@ void ffn_product(FfnLaunch l) {
     const int grp = wave >> 2;
     Frags f;
     set_a(0);
-    issue_a(a0);
+    issue_a(whole, a0);
     if constexpr (BC) {
-      set_b(0); issue_b(b0);
-      set_b(1); issue_b(b1);
-      set_b(2); issue_b(b2);
+      set_b(0); issue_b(whole, b0);
+      set_b(1); issue_b(whole, b1);
+      set_b(2); issue_b(whole, b2);
     } else {
-      set_b(0); issue_b(b0);
+      set_b(0); issue_b(whole, b0);
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(BC ? 2 * LBF : 0));
     barrier();
@@ -351,16 +368,16 @@ void ffn_product(FfnLaunch l) {
       auto loads = [&]() {
         if constexpr (EVEN) {
           set_a(j + 2);
-          issue_a(a_arr(GE_I((S + 2) % 4 / 2)));
+          issue_a(whole, a_arr(GE_I((S + 2) % 4 / 2)));
           if constexpr (!BC) {
             set_b(j + 2);
-            issue_b(b_arr(GE_I((S + 2) % 4 / 2)));
+            issue_b(whole, b_arr(GE_I((S + 2) % 4 / 2)));
           }
         } else if constexpr (BC) {
           set_b(j + 2);
-          issue_b(b_arr(GE_I((S + 2) % 4)));
+          issue_b(whole, b_arr(GE_I((S + 2) % 4)));
           set_b(j + 3);
-          issue_b(b_arr(GE_I((S + 3) % 4)));
+          issue_b(whole, b_arr(GE_I((S + 3) % 4)));
         }
       };
       if constexpr (!BC) loads();
@@ -397,9 +414,9 @@ void ffn_product(FfnLaunch l) {
     constexpr int NS = T::NSLOT, L = T::LA + LBF;
     auto fill = [&](auto i_c, int s) {
       set_a(2 * s);
-      issue_a(a_arr(i_c));
+      issue_a(whole, a_arr(i_c));
       set_b(2 * s);
-      issue_b(b_arr(i_c));
+      issue_b(whole, b_arr(i_c));
     };
     fill(GE_I(0), slot0);
     if constexpr (NS > 2) fill(GE_I(1), slot0 + 1);
@@ -434,6 +451,9 @@ void ffn_product(FfnLaunch l) {
       if constexpr (NS > 4) turn(GE_I(4), s + 4);
     }
   }
+  };
+  if (AC || K % 64 == 0) run(std::true_type{});         // (column operands need no masks)
+  else run(std::false_type{});
 #undef GE_I
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));      // loads past the end, last fragment reads
   __syncthreads();                                     // every wave is done with the slots
@@ -542,15 +562,22 @@ void ffn_product(FfnLaunch l) {
   } else if constexpr (MODE == FFN_GRAD) {
     const __amdgpu_buffer_rsrc_t du_rs = out_rs(p.Y2, p.ldy2), h_rs = out_rs(p.Y3, p.ldy2);
     const __amdgpu_buffer_rsrc_t g_rs = out_rs(const_cast<uint16_t*>(p.E1), p.lde), u_rs = out_rs(const_cast<uint16_t*>(p.E2), p.lde);
-#pragma unroll
-    for (int j = 0; j < T::FM / 2; ++j) {
-      u32x2_t gv[PASSES], uv[PASSES];
+    // the next block's G and U are on their way while this one is computed
+    u32x2_t gb[2][PASSES], ub[2][PASSES];
+    auto fetch = [&](int j) {
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps) {
         const uint32_t off = offset(wm0 + 32 * j + ps * RPP + p2_row, p.lde);
-        gv[ps] = __builtin_amdgcn_raw_buffer_load_b64(g_rs, off, 0, 0);
-        uv[ps] = __builtin_amdgcn_raw_buffer_load_b64(u_rs, off, 0, 0);
+        gb[j & 1][ps] = __builtin_amdgcn_raw_buffer_load_b64(g_rs, off, 0, 2);
+        ub[j & 1][ps] = __builtin_amdgcn_raw_buffer_load_b64(u_rs, off, 0, 2);
       }
+    };
+    fetch(0);
+#pragma unroll
+    for (int j = 0; j < T::FM / 2; ++j) {
+      if (j + 1 < T::FM / 2) fetch(j + 1);
+      const u32x2_t (&gv)[PASSES] = gb[j & 1];
+      const u32x2_t (&uv)[PASSES] = ub[j & 1];
       stage(j, [&](int i, int r, int e) { return acc[0][i][r][e]; });
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps) {
@@ -561,8 +588,9 @@ void ffn_product(FfnLaunch l) {
         for (int e = 0; e < 4; ++e) {
           const float g = (e & 1) ? bf16_hi(gv[ps][e >> 1]) : bf16_lo(gv[ps][e >> 1]);
           const float u = (e & 1) ? bf16_hi(uv[ps][e >> 1]) : bf16_lo(uv[ps][e >> 1]);
-          const float a = activate<ACT>(g);
-          dg[e] = t[e] * u * slope<ACT>(g);
+          float a, sl;
+          act_and_slope<ACT>(g, a, sl);
+          dg[e] = t[e] * u * sl;
           du[e] = t[e] * a;
           h[e] = a * u;
         }
