@@ -52,6 +52,14 @@ struct FTile {
   static_assert(NSLOT >= 2 && NSLOT <= 5, "slot arrays");
 };
 
+// Chunk swizzle of a row operand's staged row: chunk c of row r lies at c ^ (r & 6).  A 16-byte LDS
+// read serves, in one pass, lanes 0-3, 12-15 and 20-27 (then 4-11, 16-19, 28-31; the same above 32): with
+// K chunk c for lanes 0-15 and c ^ 1 for lanes 16-31, the even rows of the first set (0 2 12 14 at c, 4 6 8 10
+// at c ^ 1) fall on the even, the others on the odd chunks, and no two on one bank.  (Measured:
+// SQ_LDS_BANK_CONFLICT 1.4e8 of 2.7e8 LDS cycles on the two-row-operand product with a swizzle that
+// separates lanes 0-15 instead.)
+__device__ __forceinline__ uint32_t swz_row(uint32_t r) { return r & 6u; }
+
 // Chunk swizzle of a column operand's staged row k (see swz_b16); rows of eight chunks have no
 // fourth chunk bit to flip.
 template <int CHUNKS>
@@ -192,7 +200,7 @@ void ffn_product(FfnLaunch l) {
   // ---- direct loads: per-lane offsets, fixed for the whole loop ----
   // row operand, load u of a slot: rows 8u .. 8u+7, lane -> row lane / 8, physical chunk lane % 8
   // column operand, load u: rows u * RPL .. of the slot or stage, CHUNKS lanes per row
-  const uint32_t r_x = (uint32_t)((lane & 7) ^ (lane >> 3));
+  const uint32_t r_x = (uint32_t)(lane & 7) ^ swz_row((uint32_t)(lane >> 3));     // its logical chunk
   constexpr int ACH = T::BM / 8, BCH = T::BN / 8;      // chunks per staged row of a column operand
   uint32_t a_voff[T::LA], b_voff[T::LB];
 #pragma unroll
@@ -202,7 +210,7 @@ void ffn_product(FfnLaunch l) {
       const uint32_t row = u * (64 / ACH) + (uint32_t)lane / ACH, c = ((uint32_t)lane % ACH) ^ swz_col<ACH>(row);
       a_voff[t] = (int)(c * 8) < mrows ? row * lda2 + c * 16u : kOOB;
     } else {
-      a_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * lda2 + (r_x ^ (u & 3u)) * 16u;
+      a_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * lda2 + r_x * 16u;
     }
   }
   // loads of one B fill: a slot (LB per wave), or a 32-deep stage (LB / 2) in the two-wave loop
@@ -216,38 +224,32 @@ void ffn_product(FfnLaunch l) {
       const uint32_t row = u * (64 / BCH) + (uint32_t)lane / BCH, c = ((uint32_t)lane % BCH) ^ swz_col<BCH>(row);
       b_voff[t] = (int)(c * 8) < ncols ? row * ldb2 + c * 16u : kOOB;
     } else {
-      b_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * ldb2 + (r_x ^ (u & 3u)) * 16u;
+      b_voff[t] = (8u * u + (uint32_t)(lane >> 3)) * ldb2 + r_x * 16u;
     }
   }
   // Row operands whose K is not a multiple of a slot: chunks past K get the out-of-range offset.
-  // The chunk index is recomputed per fill (its input is opaque): kept in registers across the loop it
-  // spills the 256-row tiles.  With K a multiple of 64 (WHOLE) a slot is inside K or its extent is
-  // empty: the loop without the masks' vector instructions is 10-20 % faster on two row operands.
-  auto chunk_base = [&]() {
-    uint32_t x = r_x;
-    asm volatile("" : "+v"(x));
-    return x;
-  };
+  // With K a multiple of 64 (WHOLE) a slot is inside K or its extent is empty: the loop without the
+  // masks' vector instructions is up to 10 % faster on two row operands.
   auto issue_a = [&](auto whole, unsigned char* slot) {
     constexpr bool MASK = !AC && !decltype(whole)::value;
-    const uint32_t x = MASK ? chunk_base() : 0u;
+    const bool in_k = (int)(r_x * 8u) < a_lim;
 #pragma unroll
     for (int t = 0; t < T::LA; ++t) {
       const uint32_t u = (uint32_t)(wave * T::LA + t);
       uint32_t off = a_voff[t];
-      if constexpr (MASK) off = (int)((x ^ (u & 3u)) * 8u) < a_lim ? off : kOOB;
+      if constexpr (MASK) off = in_k ? off : kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (__attribute__((address_space(3))) void*)(slot + u * 1024), 16, off,
                                                0, 0, 0);
     }
   };
   auto issue_b = [&](auto whole, unsigned char* dst) {
     constexpr bool MASK = !BC && !decltype(whole)::value;
-    const uint32_t x = MASK ? chunk_base() : 0u;
+    const bool in_k = (int)(r_x * 8u) < b_lim;
 #pragma unroll
     for (int t = 0; t < LBF; ++t) {
       const uint32_t g = (uint32_t)(wave * LBF + t), u = g % (uint32_t)B_UNITS;   // wave-uniform
       uint32_t off = b_voff[t];
-      if constexpr (MASK) off = (int)((x ^ (u & 3u)) * 8u) < b_lim ? off : kOOB;
+      if constexpr (MASK) off = in_k ? off : kOOB;
       if (PAIR && g >= (uint32_t)B_UNITS)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(brs2, (__attribute__((address_space(3))) void*)(dst + g * 1024), 16, off,
                                                  0, 0, 0);
@@ -258,19 +260,15 @@ void ffn_product(FfnLaunch l) {
   };
 
   // ---- fragments: a lane holds K 8 * (lane / 16) .. +7 of row (column) lane % 16 of a block ----
-  // row operand: chunk 4h + lane / 16 of the staged row (h: which half of the slot); the swizzle
-  // depends on the row mod 32, so blocks of even and odd index have a base each
-  uint32_t ar[2][2], br[2][2];
+  // row operand: chunk 4h + lane / 16 of the staged row (h: which half of the slot); blocks of 16 rows
+  // are immediate offsets
+  uint32_t ar[2], br[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      const uint32_t r = 16u * (uint32_t)par + l16;
-      // a wave's first row is a multiple of 32 (A), or of 16 (B, 16-column waves): its own parity
-      const uint32_t ra = (uint32_t)wm0 + r, rb = (uint32_t)wn0 + r;
-      ar[h][par] = ra * 128u + (((4u * (uint32_t)h + q16) ^ swz_a(ra & 31u)) << 4);
-      br[h][par] = rb * 128u + (((4u * (uint32_t)h + q16) ^ swz_a(rb & 31u)) << 4);
-    }
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = ((4u * (uint32_t)h + q16) ^ swz_row(l16)) << 4;
+    ar[h] = ((uint32_t)wm0 + l16) * 128u + c;
+    br[h] = ((uint32_t)wn0 + l16) * 128u + c;
+  }
   // column operand: in each group of 16 lanes, lane s points at rows 8 q + s / 4 (and + 4) and
   // columns nb + 4 (s % 4) .. +3, and receives column nb + s of the four rows
   const uint32_t k16 = 8u * q16 + (l16 >> 2);
@@ -303,7 +301,7 @@ void ffn_product(FfnLaunch l) {
 #pragma unroll
     for (int i = 0; i < T::FM; ++i) {
       if constexpr (AC) f.a[i] = tr_read(as + ac[i] + h * 32 * (T::BM * 2), T::BM * 2);
-      else f.a[i] = *(const bf16x8_t*)(as + ar[h][i & 1] + (i >> 1) * 32 * 128);
+      else f.a[i] = *(const bf16x8_t*)(as + ar[h] + i * 16 * 128);
     }
 #pragma unroll
     for (int op = 0; op < NB; ++op)
@@ -313,7 +311,7 @@ void ffn_product(FfnLaunch l) {
           constexpr int opb = BSTAGE ? T::B_OP / 2 : T::B_OP;
           f.b[op][i] = tr_read(bs + bc[i] + op * opb + (BSTAGE ? 0 : h * 32 * (T::BN * 2)), T::BN * 2);
         } else {
-          f.b[op][i] = *(const bf16x8_t*)(bs + br[h][i & 1] + (i >> 1) * 32 * 128 + op * T::B_OP);
+          f.b[op][i] = *(const bf16x8_t*)(bs + br[h] + i * 16 * 128 + op * T::B_OP);
         }
       }
   };
