@@ -32,8 +32,10 @@ constexpr int64_t kMaxSize = 0x7FFFFFFF - 512;
 // A row operand's buffer spans up to 256 rows of one leading dimension in 31-bit byte offsets.
 constexpr int64_t kMaxLd = int64_t(1) << 22;
 
-// Rows up to which the forward products run split over the contraction instead of in tiles.
-constexpr int64_t kFewRows = 32;
+// Up to 16 rows the forward products of large weights stream them through registers instead of tiles
+// (4096 x 11008, one row: 53 us against 68 in tiles, 16 rows 58 against 70; 2048 x 5632: 23 against 29;
+// 1024 x 2816: equal; 256 x 512: 10-14 against 10, and with 24 rows the tiles win or are even).
+constexpr int64_t kFewWeights = int64_t(8) << 20;
 // A tile's contraction is split over at most this many workgroups, and only in launches of at most
 // this many in all (three on every compute unit).
 constexpr int kMaxSplits = 16;
@@ -89,23 +91,21 @@ bool add(ge::FfnLaunch& l, ge::FfnProduct p, const Choice& c, bool pair) {
   return true;
 }
 
-// Few rows: how a product is split.  Row groups of 16 or 32 rows; one workgroup of eight waves on
-// every compute unit at most, and no more splits than the longest wave's share needs.
-struct FewPlan { int rows, row_groups, tiles, splits; };
-FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
+// Few rows: how a product is split.  One workgroup of eight waves on every compute unit at most, and
+// no more splits than the longest wave's share needs.
+struct FewPlan { int tiles, splits; };
+FewPlan few_plan(int64_t N, int64_t K) {
   FewPlan f;
-  f.rows = M <= 16 ? 16 : 32;
-  f.row_groups = (int)ceil_div(M, f.rows);
   f.tiles = (int)ceil_div(N, ge::kFfnFewCols);
   const int64_t units = ceil_div(K, ge::kFfnFewUnit), waves = 8;
-  const int64_t most = std::max<int64_t>(1, 256 / std::max<int64_t>((int64_t)f.tiles * f.row_groups, 1));
+  const int64_t most = std::max<int64_t>(1, 256 / std::max<int64_t>(f.tiles, 1));
   const int64_t share = std::max<int64_t>(1, ceil_div(units, waves * most));     // units of the longest wave
   f.splits = (int)std::max<int64_t>(1, ceil_div(units, waves * share));
   return f;
 }
-size_t few_ctr_bytes(const FewPlan& f) { return (size_t)f.tiles * f.row_groups * ge::kFfnCtrStride * 4; }
+size_t few_ctr_bytes(const FewPlan& f) { return (size_t)f.tiles * ge::kFfnCtrStride * 4; }
 size_t few_part_bytes(const FewPlan& f, int operands) {
-  return f.splits > 1 ? (size_t)f.tiles * f.row_groups * f.splits * operands * f.rows * ge::kFfnFewCols * 4 : 0;
+  return f.splits > 1 ? (size_t)f.tiles * f.splits * operands * ge::kFfnFewRows * ge::kFfnFewCols * 4 : 0;
 }
 
 size_t hidden_bytes(const ge_ffn_desc_t& d) { return (size_t)d.M * (size_t)d.h * 2; }
@@ -115,9 +115,9 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // tickets come first and take the same room in both, so one workspace may serve both in turn; the
 // launches of a call follow each other and use the tickets and the partial sums in turn.
 struct Layout { size_t part, hidden, total; };
-bool few_rows(const ge_ffn_desc_t& d) { return d.tile == 0 && d.M <= kFewRows && d.d > 0 && d.h > 0; }
-FewPlan few_up(const ge_ffn_desc_t& d) { return few_plan(d.M, d.h, d.d); }
-FewPlan few_down(const ge_ffn_desc_t& d) { return few_plan(d.M, d.d, d.h); }
+bool few_rows(const ge_ffn_desc_t& d) { return d.tile == 0 && d.M <= ge::kFfnFewRows && d.d * d.h >= kFewWeights; }
+FewPlan few_up(const ge_ffn_desc_t& d) { return few_plan(d.h, d.d); }
+FewPlan few_down(const ge_ffn_desc_t& d) { return few_plan(d.d, d.h); }
 size_t ticket_bytes(const ge_ffn_desc_t& d) {
   size_t b = (size_t)kMaxSplitGroups * ge::kFfnCtrStride * 4;
   if (few_rows(d)) b = std::max({b, few_ctr_bytes(few_up(d)), few_ctr_bytes(few_down(d))});
@@ -261,7 +261,7 @@ ge_status_t ge_ffn_forward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* stre
     q.part = reinterpret_cast<float*>(ws + lay.part); q.ctr = reinterpret_cast<uint32_t*>(ws);
     q.lda = d.ldx; q.ldb = d.ldw; q.ldy = d.h; q.ldy2 = d.ldg;
     q.M = (int32_t)d.M; q.N = (int32_t)d.h; q.K = (int32_t)d.d;
-    q.tiles = f.tiles; q.splits = f.splits; q.rows = f.rows; q.row_groups = f.row_groups;
+    q.tiles = f.tiles; q.splits = f.splits;
     if (ge::launch_ffn_few(true, d.act, nk, q, s) != hipSuccess) return GE_ERR_HIP;
     f = few_down(d);
     q = ge::FfnFew{};
@@ -269,7 +269,7 @@ ge_status_t ge_ffn_forward(ge_ffn_handle_t h, const ge_ffn_args_t* a, void* stre
     q.part = reinterpret_cast<float*>(ws + lay.part); q.ctr = reinterpret_cast<uint32_t*>(ws);
     q.lda = d.h; q.ldb = d.ldwd; q.lde = d.ldr; q.ldy = d.ldy;
     q.M = (int32_t)d.M; q.N = (int32_t)d.d; q.K = (int32_t)d.h;
-    q.tiles = f.tiles; q.splits = f.splits; q.rows = f.rows; q.row_groups = f.row_groups;
+    q.tiles = f.tiles; q.splits = f.splits;
     return ge::launch_ffn_few(false, ge::ACT_NONE, nk, q, s) == hipSuccess ? GE_OK : GE_ERR_HIP;
   }
   ge::FfnLaunch pair{}, down{};

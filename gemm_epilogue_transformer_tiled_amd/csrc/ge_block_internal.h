@@ -41,16 +41,17 @@ inline FfnTileInfo ffn_tile_info(int tile) {
                                                                           : FfnTileInfo{64, 64, 64};
 }
 
-// Few rows: products split over the contraction (ge_ffn_few.hip).
+// Up to kFfnFewRows rows: products split over the contraction (ge_ffn_few.hip).
 struct FfnFew {
   const uint16_t *A, *B, *B2, *E1;
   uint16_t *Y, *Y2, *Y3;
-  float* part;                        // [tile][row group][split][operand][rows][kFfnFewCols]
-  uint32_t* ctr;                      // tickets per tile and row group, zero between calls
+  float* part;                        // [tile][split][operand][kFfnFewRows][kFfnFewCols]
+  uint32_t* ctr;                      // tickets per tile, zero between calls
   int64_t lda, ldb, lde, ldy, ldy2;
   int32_t M, N, K;
-  int32_t tiles, splits, rows, row_groups;   // rows of a row group: 16 or 32
+  int32_t tiles, splits;
 };
+constexpr int kFfnFewRows = 16;
 constexpr int kFfnFewCols = 128;
 constexpr int kFfnFewUnit = 64;              // K values a wave takes at a time
 hipError_t launch_ffn_few(bool pair, int act, bool b_nk, const FfnFew& p, hipStream_t s);

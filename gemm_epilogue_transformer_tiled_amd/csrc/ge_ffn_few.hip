@@ -1,10 +1,11 @@
 // Gated feed-forward block, few rows (decoding): the gate/up pair and the down projection.
 //
-// With few rows the products are one pass over the weights: what bounds them is how many of the
+// With up to 16 rows the products are one pass over the weights: what bounds them is how many of the
 // weights' bytes are in flight.  So a tile is 128 columns of weights, and the contraction is split
-// over the four waves of a workgroup and over several workgroups until every compute unit holds
-// two; each wave streams its part of the weights straight into registers, two 32-deep steps ahead, and
-// multiplies it with up to 32 rows by v_mfma_f32_16x16x32_bf16.  No LDS is used on the way:
+// over the eight waves of a workgroup and over several workgroups, at most one a compute unit (a second
+// one on some of them only makes the others wait); each wave streams its part of the weights straight
+// into registers, one step ahead, and multiplies it with the rows by v_mfma_f32_16x16x32_bf16.  One row
+// at 4096 x 11008: 53 us for 270 MB, [in][out]; 59 us [out][in].  No LDS is used on the way:
 //   [N][K] weights   a lane's 16 bytes are the eight K values of one column that the matrix core
 //                    wants from it
 //   [K][N] weights   a lane loads eight rows of eight columns; pairing the rows' halves (32 byte
@@ -24,44 +25,35 @@ constexpr int kFewCols = kFfnFewCols;
 // the policy loses the second half (39 -> 47 us for the pair).
 constexpr int kStream = 2;
 
-// Waves of a workgroup: two on each SIMD where their registers allow it (the pair with 32 rows holds
-// twice the sums).
-constexpr int few_waves(bool pair, int rb) { return pair && rb > 1 ? 4 : 8; }
-
-template <int ACT, bool PAIR, bool BNK, int RB>
-__global__ __launch_bounds__(64 * few_waves(PAIR, RB)) __attribute__((amdgpu_waves_per_eu(few_waves(PAIR, RB) / 4)))
+template <int ACT, bool PAIR, bool BNK>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2)))
 void ffn_few(FfnFew p) {
-  constexpr int NB = PAIR ? 2 : 1, ROWS = 16 * RB, LD = kFewCols + 4, WV = few_waves(PAIR, RB);
+  constexpr int NB = PAIR ? 2 : 1, ROWS = kFfnFewRows, LD = kFewCols + 4, WV = 8;
   __shared__ __attribute__((aligned(16))) float sums[WV * ROWS * LD];
   __shared__ uint32_t last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t l16 = (uint32_t)(lane & 15), q16 = (uint32_t)(lane >> 4);
 
-  // workgroups that read the same weights for different rows follow each other on one XCD
-  const int id = blockIdx.x, rg = id / kXCDs % p.row_groups, ts = id / (kXCDs * p.row_groups) * kXCDs + id % kXCDs;
-  if (ts >= p.tiles * p.splits) return;                // uniform: the grid is rounded up to the XCDs
-  const int tile = ts / p.splits, split = ts - tile * p.splits;
-  const int n0 = tile * kFewCols, m0 = rg * ROWS;
-  const int M = p.M, N = p.N, K = p.K;
-  const int mrows = min(M - m0, ROWS), ncols = min(N - n0, kFewCols);
+  const int tile = blockIdx.x / p.splits, split = blockIdx.x - tile * p.splits;
+  const int n0 = tile * kFewCols;
+  const int mrows = p.M, N = p.N, K = p.K;
+  const int ncols = min(N - n0, kFewCols);
   // the contraction in units of UNIT values, dealt to the waves of the splits in turn
   constexpr int UNIT = kFfnFewUnit;
   const int units = (K + UNIT - 1) / UNIT;
   const int u0 = (int)((int64_t)units * split / p.splits), u1 = (int)((int64_t)units * (split + 1) / p.splits);
 
   const uint32_t ldx2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
-  const uint16_t* const px = p.A + (int64_t)m0 * p.lda;
+  const uint16_t* const px = p.A;
   const int64_t b_at = BNK ? (int64_t)n0 * p.ldb : (int64_t)n0;
   const uint16_t* const pw[2] = {p.B + b_at, PAIR ? p.B2 + b_at : p.B + b_at};
   // block c of a lane: row l16; columns 16 c + 4 q16 + e ([N][K]), 32 q16 + 8 e + c ([K][N])
-  f32x4_t acc[NB][RB][8];
+  f32x4_t acc[NB][8];
 #pragma unroll
   for (int op = 0; op < NB; ++op)
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) acc[op][r][c] = f32x4_t{};
+    for (int c = 0; c < 8; ++c) acc[op][c] = f32x4_t{};
   auto mac = [&](const u32x4_t& w, const u32x4_t& x, f32x4_t& c) {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), __builtin_bit_cast(bf16x8_t, x), c, 0, 0, 0);
   };
@@ -74,17 +66,14 @@ void ffn_few(FfnFew p) {
     // A unit is 64 K values of all 128 columns, in two steps of four 16-column blocks: a load takes
     // 64 bytes of 16 rows, the two loads of a block a whole cache line of each
     struct W { u32x4_t v[NB][4][2]; };
-    struct X { u32x4_t v[RB][2]; };
+    struct X { u32x4_t v[2]; };
     const uint32_t x_off = l16 * ldx2 + q16 * 16u, w_off = l16 * ldb2 + q16 * 16u;
     auto load_x = [&](X& t, int u) {
       const int k0 = u * UNIT, lim = u < u1 ? K - k0 : 0;
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(px + k0, lim > 0 ? (mrows - 1) * (int)ldx2 + lim * 2 : 0);
 #pragma unroll
-      for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          t.v[r][j] = __builtin_amdgcn_raw_buffer_load_b128(
-              rs, (int)(q16 * 8u) + 32 * j < lim ? x_off + (uint32_t)r * 16u * ldx2 + 64u * j : kOOB, 0, 0);
+      for (int j = 0; j < 2; ++j)
+        t.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(q16 * 8u) + 32 * j < lim ? x_off + 64u * j : kOOB, 0, 0);
     };
     auto load_w = [&](W& t, int u, int cp) {
       const int k0 = u * UNIT, lim = u < u1 ? K - k0 : 0;
@@ -106,9 +95,7 @@ void ffn_few(FfnFew p) {
 #pragma unroll
         for (int op = 0; op < NB; ++op)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int r = 0; r < RB; ++r) mac(w.v[op][i][j], x.v[r][j], acc[op][r][4 * CP + i]);
+          for (int i = 0; i < 4; ++i) mac(w.v[op][i][j], x.v[j], acc[op][4 * CP + i]);
     };
     // Each tile starts its units at a place of its own: all rows have the same pitch, and if the tiles
     // walked K in step, a power-of-two pitch would put what they read at a time on a few of the
@@ -135,16 +122,13 @@ void ffn_few(FfnFew p) {
     }
   } else {
     // A unit is two 32-deep steps; a lane's step is eight rows of eight columns.
-    struct Step { u32x4_t w[NB][8], x[RB]; };
+    struct Step { u32x4_t w[NB][8], x; };
     const uint32_t x_off = l16 * ldx2 + q16 * 16u;
     const uint32_t w_off = (int)(l16 * 8u) < ncols ? 8u * q16 * ldb2 + l16 * 16u : kOOB;
     auto load = [&](Step& t, int u, int half) {
       const int k0 = u * UNIT + 32 * half, lim = u < u1 ? K - k0 : 0;      // past the split's end: zeros
       const __amdgpu_buffer_rsrc_t xr = make_rsrc(px + k0, lim > 0 ? (mrows - 1) * (int)ldx2 + lim * 2 : 0);
-      const bool in_k = (int)(q16 * 8u) < lim;
-#pragma unroll
-      for (int r = 0; r < RB; ++r)
-        t.x[r] = __builtin_amdgcn_raw_buffer_load_b128(xr, in_k ? x_off + (uint32_t)r * 16u * ldx2 : kOOB, 0, 0);
+      t.x = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(q16 * 8u) < lim ? x_off : kOOB, 0, 0);
 #pragma unroll
       for (int op = 0; op < NB; ++op) {
         const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char*)pw[op] + (uint64_t)(uint32_t)k0 * ldb2,
@@ -163,8 +147,7 @@ void ffn_few(FfnFew p) {
           for (int j = 0; j < 4; ++j)
             f[j] = __builtin_amdgcn_perm(t.w[op][2 * j + 1][c >> 1], t.w[op][2 * j][c >> 1],
                                          (c & 1) ? 0x07060302u : 0x05040100u);
-#pragma unroll
-          for (int r = 0; r < RB; ++r) mac(f, t.x[r], acc[op][r][c]);
+          mac(f, t.x, acc[op][c]);
         }
     };
     Step a, b;
@@ -190,20 +173,17 @@ void ffn_few(FfnFew p) {
 #pragma unroll
   for (int op = 0; op < NB; ++op) {
     if (op > 0) __syncthreads();
+    float* row = sums + (wave * ROWS + (int)l16) * LD;
+    if constexpr (BNK) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float* row = sums + (wave * ROWS + 16 * r + (int)l16) * LD;
-      if constexpr (BNK) {
+      for (int c = 0; c < 8; ++c) *(f32x4_t*)(row + 16 * c + 4 * (int)q16) = acc[op][c];
+    } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) *(f32x4_t*)(row + 16 * c + 4 * (int)q16) = acc[op][r][c];
-      } else {
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *(f32x4_t*)(row + 32 * (int)q16 + 8 * e + 4 * h) =
-                f32x4_t{acc[op][r][4 * h][e], acc[op][r][4 * h + 1][e], acc[op][r][4 * h + 2][e], acc[op][r][4 * h + 3][e]};
-      }
+        for (int h = 0; h < 2; ++h)
+          *(f32x4_t*)(row + 32 * (int)q16 + 8 * e + 4 * h) =
+              f32x4_t{acc[op][4 * h][e], acc[op][4 * h + 1][e], acc[op][4 * h + 2][e], acc[op][4 * h + 3][e]};
     }
     __syncthreads();
 #pragma unroll
@@ -219,8 +199,7 @@ void ffn_few(FfnFew p) {
   // (the partials are performed before the ticket; the last workgroup reads them after it) ----
   if (p.splits > 1) {
     typedef unsigned long long u64;
-    const int slot = tile * p.row_groups + rg;
-    u64* mine = (u64*)(p.part + ((int64_t)slot * p.splits + split) * (NB * ROWS * kFewCols));
+    u64* mine = (u64*)(p.part + ((int64_t)tile * p.splits + split) * (NB * ROWS * kFewCols));
 #pragma unroll
     for (int op = 0; op < NB; ++op)
 #pragma unroll
@@ -235,7 +214,7 @@ void ffn_few(FfnFew p) {
     __builtin_amdgcn_s_waitcnt(kVmcnt0);
     __syncthreads();
     if (tid == 0) {
-      uint32_t* ctr = p.ctr + (uint32_t)slot * kFfnCtrStride;
+      uint32_t* ctr = p.ctr + (uint32_t)tile * kFfnCtrStride;
       const bool l = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)p.splits - 1u;
       if (l) __hip_atomic_store(ctr, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       last = l ? 1u : 0u;
@@ -243,8 +222,8 @@ void ffn_few(FfnFew p) {
     __syncthreads();
     if (!last) return;                                 // uniform
     // every element's partials of AHEAD splits are on their way at once, added in split order
-    const u64* all = (const u64*)(p.part + (int64_t)slot * p.splits * (NB * ROWS * kFewCols));
-    constexpr int AHEAD = NB * PER >= 8 ? 2 : 4;
+    const u64* all = (const u64*)(p.part + (int64_t)tile * p.splits * (NB * ROWS * kFewCols));
+    constexpr int AHEAD = 4;
 #pragma unroll
     for (int op = 0; op < NB; ++op)
 #pragma unroll
@@ -287,8 +266,8 @@ void ffn_few(FfnFew p) {
   };
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int r = tr + RS * i, row = m0 + r;
-    if (r >= mrows) continue;
+    const int row = tr + RS * i;
+    if (row >= mrows) continue;
     if constexpr (PAIR) {
       f32x4_t h;
 #pragma unroll
@@ -313,21 +292,18 @@ void ffn_few(FfnFew p) {
 }
 
 template <int ACT, bool PAIR, bool BNK>
-hipError_t by_rows(const FfnFew& p, hipStream_t s) {
-  const unsigned ts = (unsigned)((p.tiles * p.splits + kXCDs - 1) / kXCDs * kXCDs);
-  const dim3 grid(ts * (unsigned)p.row_groups);
-  if (p.rows == 16) hipLaunchKernelGGL((ffn_few<ACT, PAIR, BNK, 1>), grid, dim3(64 * few_waves(PAIR, 1)), 0, s, p);
-  else hipLaunchKernelGGL((ffn_few<ACT, PAIR, BNK, 2>), grid, dim3(64 * few_waves(PAIR, 2)), 0, s, p);
+hipError_t go(const FfnFew& p, hipStream_t s) {
+  hipLaunchKernelGGL((ffn_few<ACT, PAIR, BNK>), dim3((unsigned)(p.tiles * p.splits)), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
 template <bool BNK>
 hipError_t by_act(int act, const FfnFew& p, hipStream_t s) {
   switch (act) {
-    case ACT_NONE: return by_rows<ACT_NONE, true, BNK>(p, s);
-    case ACT_RELU: return by_rows<ACT_RELU, true, BNK>(p, s);
-    case ACT_GELU_TANH: return by_rows<ACT_GELU_TANH, true, BNK>(p, s);
-    case ACT_SILU: return by_rows<ACT_SILU, true, BNK>(p, s);
+    case ACT_NONE: return go<ACT_NONE, true, BNK>(p, s);
+    case ACT_RELU: return go<ACT_RELU, true, BNK>(p, s);
+    case ACT_GELU_TANH: return go<ACT_GELU_TANH, true, BNK>(p, s);
+    case ACT_SILU: return go<ACT_SILU, true, BNK>(p, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -335,9 +311,9 @@ hipError_t by_act(int act, const FfnFew& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_ffn_few(bool pair, int act, bool b_nk, const FfnFew& p, hipStream_t s) {
-  if (p.tiles <= 0 || p.row_groups <= 0) return hipSuccess;
+  if (p.tiles <= 0) return hipSuccess;
   if (pair) return b_nk ? by_act<true>(act, p, s) : by_act<false>(act, p, s);
-  return b_nk ? by_rows<ACT_NONE, false, true>(p, s) : by_rows<ACT_NONE, false, false>(p, s);
+  return b_nk ? go<ACT_NONE, false, true>(p, s) : go<ACT_NONE, false, false>(p, s);
 }
 
 }  // namespace ge

@@ -181,6 +181,28 @@ def test_split_contractions(M, d, h, layout):
             assert torch.equal(first[k], again[k]), (k, plan.describe())
 
 
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("M,d,h", [(1, 2048, 4104), (2, 4104, 2056), (7, 1032, 8200), (15, 2056, 4096), (16, 2184, 4136),
+                                   (16, 8200, 1032)])
+def test_few_rows_of_large_weights(M, d, h, layout):
+    """The kernels that stream the weights through registers, with every edge: rows, columns, contraction."""
+    for act, save in (("silu", True), ("gelu_tanh", False), ("relu", True), ("none", False)):
+        c = Case(M, d, h, layout=layout, act=act, residual=save)
+        plan = c.plan(save=save)
+        assert plan.describe().startswith("few rows")
+        out = c.forward(plan=plan, save=save)
+        c.check_forward(out, act)
+        again = c.forward(plan=plan, save=save)
+        for k in out:
+            assert torch.equal(out[k], again[k]), k
+    c.check_backward(c.backward(), "backward")
+    c = Case(M, d, h, layout=layout, pad=8)
+    out = c.forward()
+    c.check_forward(out, "padded")
+    for k, v in out.items():
+        assert (v._base[:, v.shape[1]:].view(torch.int16) == NAN_BITS).all(), k
+
+
 def test_splits_are_chosen():
     """The sizes above reach the split kernels of every product (one at least each)."""
     seen = [Case(*s).plan().describe() for s in ((64, 264, 4104), (40, 2056, 264), (96, 4104, 520), (4100, 72, 136))]
