@@ -20,7 +20,7 @@ using ge::block::Matrix;
 struct ge_qk_plan {
   ge_qk_desc_t desc;
   int device;
-  int group, tokens_per_wg, head_splits, grid_forward, grid_backward;
+  int group, tokens_per_wg, head_splits, q_splits, grid_forward, grid_backward;
 };
 
 namespace {
@@ -148,6 +148,7 @@ bool fill(const ge_qk_plan* h, const ge_qk_args_t* a, bool backward, ge::QkParam
   p.group = h->group;
   p.tokens_per_wg = h->tokens_per_wg;
   p.head_splits = h->head_splits;
+  p.q_splits = h->q_splits;
   p.workgroups = backward ? h->grid_backward : h->grid_forward;
   p.pos64 = d.pos64 != 0;
   p.eps = d.eps;
@@ -208,7 +209,9 @@ ge_status_t ge_qk_create(const ge_qk_desc_t* d, ge_qk_handle_t* handle) {
   if (d->tokens * heads <= 1024 * groups) {
     // few heads in all: one head per group of lanes, so that every compute unit has work
     p->tokens_per_wg = 1;
-    p->head_splits = (int)std::max<int64_t>(1, ceil_div(std::max(d->heads_q, d->heads_k), groups));
+    p->q_splits = (int)ceil_div(d->heads_q, groups);
+    p->head_splits = p->q_splits + (int)ceil_div(d->heads_k, groups);
+    if (p->head_splits < 2) p->head_splits = 1;        // (one of the two has no heads)
   } else {
     // a workgroup turns about one angle per thread, then all heads of those tokens; fewer tokens
     // where that would leave less than four workgroups for a compute unit
@@ -216,6 +219,7 @@ ge_status_t ge_qk_create(const ge_qk_desc_t* d, ge_qk_handle_t* handle) {
     const int64_t most = std::min<int64_t>(std::max(ge::kQkThreads / rot2, 1), kMostTokens);
     p->tokens_per_wg = (int)std::min(most, std::max<int64_t>(1, d->tokens / 1024));
     p->head_splits = 1;
+    p->q_splits = 0;
   }
   const int64_t turns = heads > 0 ? ceil_div(d->tokens, p->tokens_per_wg) * p->head_splits : 0;
   p->grid_forward = (int)std::min<int64_t>(turns, 1 << 20);

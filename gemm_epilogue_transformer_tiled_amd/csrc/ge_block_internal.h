@@ -76,7 +76,8 @@ struct QkParams {
   int32_t head_dim, rot_dim;
   int32_t group;              // lanes per head: a power of two, 8 values a lane
   int32_t tokens_per_wg;      // tokens of one turn of a workgroup
-  int32_t head_splits;        // workgroups that share a token's heads
+  int32_t head_splits;        // workgroups that share a token's heads: 1, or
+  int32_t q_splits;           // q_splits for the queries' and the rest for the keys'
   int32_t workgroups;         // grid.x
   bool pos64;
   float eps, amplitude;

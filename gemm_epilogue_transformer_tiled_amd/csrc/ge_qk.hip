@@ -207,11 +207,13 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
     const int64_t t0 = it / hs * tw;
     const int part = (int)(it % hs);
     const int nt = (int)(p.tokens - t0 < tw ? p.tokens - t0 : tw);
-    // All heads of the queries, then those of the keys: which of the two is uniform.  One item (a
-    // head of a token) per group and step; the next one is loaded before this one is computed.
-    auto side = [&](auto w_c, bool angles) {
+    // The heads of the queries, then those of the keys (or, with few tokens, only some of one of
+    // them): which of the two is uniform.  One item (a head of a token) per group and step; the next
+    // one is loaded before this one is computed.
+    auto side = [&](auto w_c, bool angles, int part, int parts) {
       constexpr int w = decltype(w_c)::value;
-      const int h_lo = (int)((int64_t)p.heads[w] * part / hs), nh = (int)((int64_t)p.heads[w] * (part + 1) / hs) - h_lo;
+      const int h_lo = (int)((int64_t)p.heads[w] * part / parts);
+      const int nh = (int)((int64_t)p.heads[w] * (part + 1) / parts) - h_lo;
       const E* const px = (const E*)p.x[w] + t0 * p.xt[w] + h_lo * p.xh[w];
       const E* const pd = (const E*)p.dy[w] + t0 * p.dt[w] + h_lo * p.dh[w];
       E* const py = (E*)p.y[w] + t0 * p.yt[w] + h_lo * p.yh[w];
@@ -328,8 +330,9 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
         now = next;
       }
     };
-    side(std::integral_constant<int, 0>{}, true);
-    side(std::integral_constant<int, 1>{}, false);
+    const int qs = p.q_splits;
+    if (hs == 1 || part < qs) side(std::integral_constant<int, 0>{}, true, part, hs == 1 ? 1 : qs);
+    if (hs == 1 || part >= qs) side(std::integral_constant<int, 1>{}, hs > 1, hs == 1 ? 0 : part - qs, hs == 1 ? 1 : hs - qs);
   }
 
   if constexpr (BWD && NORM) {
