@@ -72,6 +72,7 @@ struct QkParams {
   float* part;                // backward with norm: partial gain gradients [workgroups][2][head_dim]
   int64_t xt[2], xh[2], yt[2], yh[2], dt[2], dh[2];   // token and head strides of x, y, dy
   int64_t tokens;
+  int64_t turns;              // runs of tokens_per_wg tokens, times head_splits
   int32_t heads[2];
   int32_t head_dim, rot_dim;
   int32_t group;              // lanes per head: a power of two, 8 values a lane

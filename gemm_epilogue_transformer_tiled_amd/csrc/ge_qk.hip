@@ -173,7 +173,7 @@ __device__ __forceinline__ auto head_at(int t, int h, int64_t st, int64_t sh) {
 
 template <class E, bool WIDE, bool HALF, bool NORM, bool BWD>
 __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
-  __shared__ __attribute__((aligned(16))) float2 turn[kQkMaxAngles];
+  __shared__ __attribute__((aligned(16))) float turn_c[kQkMaxAngles], turn_s[kQkMaxAngles];
   __shared__ float gsum[BWD && NORM ? 2 * 8 * kQkThreads : 1];
   const int tid = threadIdx.x, G = p.group;
   const int gl = tid & (G - 1), ng = kQkThreads / G, grp = tid / G;
@@ -202,18 +202,22 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
     Raw<E, WIDE> x, d;
   };
   const int tw = p.tokens_per_wg, hs = p.head_splits;
-  const int64_t turns = (p.tokens + tw - 1) / tw * hs;
+  // (a token's heads are split only where all heads of all tokens are few: 32-bit divisions)
+  const int64_t turns = p.turns;
   for (int64_t it = blockIdx.x; it < turns; it += gridDim.x) {
-    const int64_t t0 = it / hs * tw;
-    const int part = (int)(it % hs);
+    const int64_t t0 = hs == 1 ? it * tw : (int64_t)((uint32_t)it / (uint32_t)hs * (uint32_t)tw);
+    const int part = hs == 1 ? 0 : (int)((uint32_t)it % (uint32_t)hs);
     const int nt = (int)(p.tokens - t0 < tw ? p.tokens - t0 : tw);
     // The heads of the queries, then those of the keys (or, with few tokens, only some of one of
     // them): which of the two is uniform.  One item (a head of a token) per group and step; the next
     // one is loaded before this one is computed.
     auto side = [&](auto w_c, bool angles, int part, int parts) {
       constexpr int w = decltype(w_c)::value;
-      const int h_lo = (int)((int64_t)p.heads[w] * part / parts);
-      const int nh = (int)((int64_t)p.heads[w] * (part + 1) / parts) - h_lo;
+      int h_lo = 0, nh = p.heads[w];
+      if (parts > 1) {
+        h_lo = (int)((uint32_t)p.heads[w] * (uint32_t)part / (uint32_t)parts);
+        nh = (int)((uint32_t)p.heads[w] * (uint32_t)(part + 1) / (uint32_t)parts) - h_lo;
+      }
       const E* const px = (const E*)p.x[w] + t0 * p.xt[w] + h_lo * p.xh[w];
       const E* const pd = (const E*)p.dy[w] + t0 * p.dt[w] + h_lo * p.dh[w];
       E* const py = (E*)p.y[w] + t0 * p.yt[w] + h_lo * p.yh[w];
@@ -237,17 +241,16 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
         float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (WIDE) {
           if (slot < rot2) {
-            const f32x4 u = *(const f32x4*)(turn + t * rot2 + slot), v = *(const f32x4*)(turn + t * rot2 + slot + 2);
-            cs[0] = u[0]; sn[0] = u[1]; cs[1] = u[2]; sn[1] = u[3];
-            cs[2] = v[0]; sn[2] = v[1]; cs[3] = v[2]; sn[3] = v[3];
+            const f32x4 u = *(const f32x4*)(turn_c + t * rot2 + slot), v = *(const f32x4*)(turn_s + t * rot2 + slot);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { cs[j] = u[j]; sn[j] = v[j]; }
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (slot + j < rot2) {
-              const float2 a = turn[t * rot2 + slot + j];
-              cs[j] = a.x;
-              sn[j] = a.y;
+              cs[j] = turn_c[t * rot2 + slot + j];
+              sn[j] = turn_s[t * rot2 + slot + j];
             }
         }
         if constexpr (!BWD) {
@@ -313,7 +316,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
           turns_of -= __builtin_rint(turns_of);
           float s, c;
           sincospif(2.0f * (float)turns_of, &s, &c);
-          turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+          turn_c[i] = c * p.amplitude;
+          turn_s[i] = s * p.amplitude;
         }
         __syncthreads();
       }

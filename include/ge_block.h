@@ -69,7 +69,9 @@ typedef struct {
 } ge_ffn_desc_t;
 
 /* Output tiles of the block's products (rows x columns of one workgroup; the gate/up pair halves
- * the columns of the largest).  Results do not depend on the tile, bit for bit. */
+ * the columns of the largest).  A requested tile sums every product in ascending order of its
+ * contraction, so that all tiles give the same bits; the library's own choice may split a long
+ * contraction over workgroups and add the parts (in a fixed order: equal calls give equal bits). */
 typedef enum { GE_FFN_TILE_256 = 0, GE_FFN_TILE_128 = 1, GE_FFN_TILE_64 = 2, GE_FFN_TILE_COUNT = 3 } ge_ffn_tile_t;
 
 typedef struct {
@@ -92,8 +94,9 @@ ge_status_t ge_ffn_validate(const ge_ffn_desc_t* desc);
 /* Validates, checks that the current device is gfx950 (GE_ERR_DEVICE) and builds the handle;
  * *out is NULL on failure. */
 ge_status_t ge_ffn_create(const ge_ffn_desc_t* desc, ge_ffn_handle_t* out);
-/* Workspace bytes of ge_ffn_forward (backward = 0: H, and the split sums of few-row calls) or
- * ge_ffn_backward (backward = 1: dG, dU and H). */
+/* Workspace bytes of ge_ffn_forward (backward = 0: H) or ge_ffn_backward (backward = 1: dG, dU and
+ * H), each with the tickets and partial sums of split contractions.  One workspace of the larger
+ * size serves both calls in turn. */
 ge_status_t ge_ffn_workspace_size(ge_ffn_handle_t handle, int32_t backward, size_t* bytes);
 /* Y (and, with desc.save, G and U) from X, the weights and R.  Two launches. */
 ge_status_t ge_ffn_forward(ge_ffn_handle_t handle, const ge_ffn_args_t* args, void* stream);
@@ -161,8 +164,8 @@ typedef struct ge_qk_plan* ge_qk_handle_t;
 
 ge_status_t ge_qk_validate(const ge_qk_desc_t* desc);
 ge_status_t ge_qk_create(const ge_qk_desc_t* desc, ge_qk_handle_t* out);
-/* Workspace bytes of ge_qk_backward (partial sums of the gains' gradients; it needs no zero fill);
- * 0 without norm.  ge_qk_forward needs none. */
+/* Workspace bytes of ge_qk_backward (partial sums of the gains' gradients, every one written by
+ * each call: it needs no zero fill); 0 without norm.  ge_qk_forward needs none. */
 ge_status_t ge_qk_workspace_size(ge_qk_handle_t handle, size_t* bytes);
 /* One launch. */
 ge_status_t ge_qk_forward(ge_qk_handle_t handle, const ge_qk_args_t* args, void* stream);
@@ -199,7 +202,8 @@ typedef struct {
 typedef struct ge_clip_plan* ge_clip_handle_t;
 
 /* tensors: host array of n entries, copied into the handle.  GE_ERR_INVALID_ARG (n < 0, NULL with
- * n > 0, a negative length, an unknown type), GE_ERR_UNSUPPORTED (2^46 values or more in all). */
+ * n > 0, a negative length, an unknown type), GE_ERR_UNSUPPORTED (fp8 values, 2^45 values or more
+ * in all, more than 32768 non-empty tensors). */
 ge_status_t ge_clip_create(const ge_clip_tensor_t* tensors, int32_t n, ge_clip_handle_t* out);
 ge_status_t ge_clip_workspace_size(ge_clip_handle_t handle, size_t* bytes);
 /* Two launches for up to 128 non-empty tensors (one more pair for each further 128). */
