@@ -130,6 +130,13 @@ class _Plan:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.handle = None
 
+    def _create(self, call, where: str) -> None:
+        """Makes the handle with the plan's device current: it belongs to that device."""
+        out = _p()
+        with torch.cuda.device(self.device):
+            _check(call(ctypes.byref(out)), where)
+        self.handle = out.value
+
     def _scratch(self, nbytes: int) -> torch.Tensor:
         """A zero-filled workspace that stays where it is as long as the plan lives (captured graphs
         hold its address)."""
@@ -215,9 +222,7 @@ class GatedFFN(_Plan):
                  save: bool = False, tile: Optional[int] = None, device="cuda", **ld: int):
         super().__init__(device)
         self.desc = make_ffn_desc(M, d, h, act, w_layout, residual, save, tile, **ld)
-        out = _p()
-        _check(lib.ge_ffn_create(ctypes.byref(self.desc), ctypes.byref(out)), "ge_ffn_create")
-        self.handle = out.value
+        self._create(lambda out: lib.ge_ffn_create(ctypes.byref(self.desc), out), "ge_ffn_create")
         # forward and backward share one workspace in a training plan; a plan without `save` whose
         # backward is called gets a second one
         self.workspace = self._scratch(max(self.workspace_size(b) for b in ((False, True) if save else (False,))))
@@ -358,9 +363,7 @@ class QKRotary(_Plan):
         self.desc = ge_qk_desc_t(tokens, heads_q, heads_k, *q, *k, *oq, *ok, *dq, *dk, head_dim,
                                  head_dim if rot_dim is None else rot_dim, PAIR_NAMES[pairs], int(norm), DTYPES[dtype],
                                  int(positions_dtype == torch.int64), eps)
-        out = _p()
-        _check(lib.ge_qk_create(ctypes.byref(self.desc), ctypes.byref(out)), "ge_qk_create")
-        self.handle = out.value
+        self._create(lambda out: lib.ge_qk_create(ctypes.byref(self.desc), out), "ge_qk_create")
         n = _sz()
         _check(lib.ge_qk_workspace_size(self.handle, ctypes.byref(n)), "ge_qk_workspace_size")
         self.workspace_bytes = n.value
@@ -439,9 +442,7 @@ class GradClip(_Plan):
                 raise ValueError(f"gradient of type {g.dtype}: bfloat16 or float32")
         self.like = [(g.numel(), g.dtype) for g in grads]
         table = (ge_clip_tensor_t * max(len(grads), 1))(*[(n, DTYPES[t]) for n, t in self.like])
-        out = _p()
-        _check(lib.ge_clip_create(table, len(grads), ctypes.byref(out)), "ge_clip_create")
-        self.handle = out.value
+        self._create(lambda out: lib.ge_clip_create(table, len(grads), out), "ge_clip_create")
         n = _sz()
         _check(lib.ge_clip_workspace_size(self.handle, ctypes.byref(n)), "ge_clip_workspace_size")
         self.workspace = self._scratch(n.value)

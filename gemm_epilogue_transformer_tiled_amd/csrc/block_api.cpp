@@ -41,6 +41,13 @@ constexpr int64_t kFewWeights = int64_t(8) << 20;
 constexpr int kMaxSplits = 16;
 constexpr int kMaxSplitGroups = 768;
 
+// Whether a launch's threads can be counted in 32 bits, which the runtime asks for.
+bool grid_fits(int tile, int64_t M, int64_t N, bool pair, int products) {
+  const ge::FfnTileInfo ti = ge::ffn_tile_info(tile);
+  const double tiles = (double)ceil_div(M, ti.bm) * (double)ceil_div(N, pair ? ti.bn_pair : ti.bn) * products;
+  return tiles * (tile == ge::FFN_T64 ? 256 : 512) <= 4294967295.0;
+}
+
 // Tile and splits of one launch: the least estimated time in microseconds.  A tile costs `fixed` and
 // `slot` for every 64 values of the contraction, `crowd` instead where workgroups share a compute
 // unit or come in rounds; a split adds the partial sums' way through memory and back.  The figures
@@ -54,9 +61,10 @@ Choice pick(int mode, int64_t M, int64_t N, int64_t K, int products, int32_t ask
   const Cost cost[ge::FFN_TILES] = {{7.0, 1.3, 1.4},
                                     {3.0, pair ? 1.0 : 0.5, pair ? 1.0 : dw ? 0.65 : 0.57},
                                     {1.5, pair ? 0.45 : 0.26, pair ? 0.43 : dw ? 0.27 : 0.21}};
-  Choice best{ge::FFN_T64, 1};
+  Choice best{ge::FFN_T256, 1};
   double least = 1e300;
   for (int t = 0; t < ge::FFN_TILES; ++t) {
+    if (!grid_fits(t, M, N, pair, products)) continue;
     const ge::FfnTileInfo ti = ge::ffn_tile_info(t);
     const int bn = pair ? ti.bn_pair : ti.bn;
     const double tiles = (double)ceil_div(M, ti.bm) * (double)ceil_div(N, bn) * products;
@@ -186,10 +194,9 @@ ge_status_t ge_ffn_validate(const ge_ffn_desc_t* d) {
   for (auto& l : lds)
     if (l[0] % 8 || l[0] >= kMaxLd) return GE_ERR_UNSUPPORTED;
   if (d->M > kMaxSize || d->d > kMaxSize || d->h > kMaxSize) return GE_ERR_UNSUPPORTED;
-  // every launch's grid in 31 bits even with the smallest tile, three products at once
-  const int64_t bm = 64;
-  if (ceil_div(d->M, bm) * ceil_div(d->h, bm) > 0x3FFFFFFF || ceil_div(d->M, bm) * ceil_div(d->d, bm) > 0x3FFFFFFF ||
-      ceil_div(d->d, bm) * ceil_div(d->h, bm) > 0x1FFFFFFF)
+  const int tile = d->tile ? d->tile - 1 : ge::FFN_T256;
+  if (!grid_fits(tile, d->M, d->h, true, 1) || !grid_fits(tile, d->M, d->h, false, 1) ||
+      !grid_fits(tile, d->M, d->d, false, 1) || !grid_fits(tile, std::max(d->d, d->h), std::min(d->d, d->h), false, 3))
     return GE_ERR_UNSUPPORTED;
   return GE_OK;
 }

@@ -49,6 +49,9 @@ def _ffn(**kw):
     (dict(ldx=1 << 22), ge.GE_ERR_UNSUPPORTED),
     (dict(M=1 << 31), ge.GE_ERR_UNSUPPORTED),
     (dict(M=(1 << 31) - 1024, h=1 << 20), ge.GE_ERR_UNSUPPORTED),   # the grid passes 31 bits
+    (dict(M=(1 << 31) - 1024, d=8, h=8), ge.GE_OK),
+    (dict(M=(1 << 31) - 1024, d=8, h=8, tile=block.GE_FFN_TILE_64), ge.GE_ERR_UNSUPPORTED),   # 2^33 threads
+    (dict(M=(1 << 31) - 1024, d=8, h=264), ge.GE_ERR_UNSUPPORTED),
     (dict(tile=3), ge.GE_ERR_INVALID_ARG),
 ])
 def test_ffn_descriptors(kw, want):
