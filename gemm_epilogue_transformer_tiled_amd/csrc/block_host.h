@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstring>
 
 namespace ge {
@@ -12,14 +13,26 @@ namespace block {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// The current device, if it is a gfx950.
+// The current device, if it is a gfx950.  What a device is does not change: its properties (some
+// 20 us to ask for) are read once.
 inline bool current_gfx950(int* device) {
-  hipDeviceProp_t prop;
-  if (hipGetDevice(device) != hipSuccess || hipGetDeviceProperties(&prop, *device) != hipSuccess) {
+  static std::atomic<int> known[64];                   // 0: not asked, 1: gfx950, 2: another
+  if (hipGetDevice(device) != hipSuccess) {
     (void)hipGetLastError();
     return false;
   }
-  return std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+  const bool kept = *device >= 0 && *device < 64;
+  int k = kept ? known[*device].load(std::memory_order_relaxed) : 0;
+  if (k == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, *device) != hipSuccess) {
+      (void)hipGetLastError();
+      return false;
+    }
+    k = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+    if (kept) known[*device].store(k, std::memory_order_relaxed);
+  }
+  return k == 1;
 }
 inline bool is_current(int device) {
   int now = -1;
