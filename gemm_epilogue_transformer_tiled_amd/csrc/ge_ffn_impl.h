@@ -23,8 +23,14 @@
 // grows with the tensors (they stay below 256 rows of one leading dimension).
 //
 // Loops.  256-row tiles: 8 waves, two per SIMD, in two groups that alternate a memory phase
-// (fragment reads, later steps' loads) and a matrix phase, as in ge_kernel_impl.h.  The smaller
-// tiles: 4 waves, a ring of NSLOT 64-deep slots, one barrier per slot, several workgroups per CU.
+// (fragment reads, later steps' loads) and a matrix phase, as in ge_kernel_impl.h; every step carries
+// 32 KB of loads.  128-row tiles: 8 waves, 64-row tiles: 4, a ring of NSLOT 64-deep slots, one barrier
+// per slot; their contraction may be split over workgroups (few tiles, long contractions).
+//
+// What bounds them (8192 x 4096 x 11008, bf16): the matrix cores under the power limit.  Forward pair
+// 1,060-1,110 us (1.33-1.39 PFLOP/s, with 540 MB of stores in the epilogue), down 509 us (1.45), input
+// gradient 975 us (1.52), weight gradients 1,600-1,680 us (1.32-1.38); the gated gradient 670 us (1.10):
+// its epilogue moves 900 MB (G, U in; dG, dU, H out) that the loop does not hide.
 #include "ge_block_internal.h"
 #include "ge_kernel_impl.h"
 
