@@ -13,7 +13,7 @@
  * graph.  Calls only read the handle, so several threads may use one handle at once, each with
  * its own outputs and workspace.
  *
- * Workspace: device scratch of the size *_workspace_size reports, 256-byte aligned, owned by the
+ * Workspace: device scratch of the size *_workspace_size reports, 16-byte aligned, owned by the
  * caller, ZERO-FILLED before its first use; each call that completes leaves its counters at zero
  * again.  HAZARD: calls that share a workspace must not overlap in time (two streams, or two
  * graphs replayed at once); give concurrent calls workspaces of their own, and clear a workspace
