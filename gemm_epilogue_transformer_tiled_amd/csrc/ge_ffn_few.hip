@@ -5,7 +5,7 @@
 // over the eight waves of a workgroup and over several workgroups, at most one a compute unit (a second
 // one on some of them only makes the others wait); each wave streams its part of the weights straight
 // into registers, one step ahead, and multiplies it with the rows by v_mfma_f32_16x16x32_bf16.  One row
-// at 4096 x 11008: 53 us for 270 MB, [in][out]; 59 us [out][in].  No LDS is used on the way:
+// at 4096 x 11008: 53 us for 270 MB, [in][out]; 58 us [out][in].  No LDS is used on the way:
 //   [N][K] weights   a lane's 16 bytes are the eight K values of one column that the matrix core
 //                    wants from it
 //   [K][N] weights   a lane loads eight rows of eight columns; pairing the rows' halves (32 byte
@@ -14,6 +14,7 @@
 // The waves' sums meet in LDS in wave order, the workgroups' in the workspace in split order (the
 // last workgroup of a tile, found by a ticket, adds them up), so equal calls give equal bits.
 #include "ge_block_internal.h"
+#include "ge_ffn_few_addr.h"
 #include "ge_kernel_impl.h"
 
 namespace ge {
@@ -67,25 +68,26 @@ void ffn_few(FfnFew p) {
     // 64 bytes of 16 rows, the two loads of a block a whole cache line of each
     struct W { u32x4_t v[NB][4][2]; };
     struct X { u32x4_t v[2]; };
-    const uint32_t x_off = l16 * ldx2 + q16 * 16u, w_off = l16 * ldb2 + q16 * 16u;
+    uint32_t column[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) column[c] = few_nk_column(l16, q16, c, ncols, ldb2);
     auto load_x = [&](X& t, int u) {
       const int k0 = u * UNIT, lim = u < u1 ? K - k0 : 0;
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc(px + k0, lim > 0 ? (mrows - 1) * (int)ldx2 + lim * 2 : 0);
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(px + k0, few_row_extent(mrows, lim, ldx2));
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        t.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(q16 * 8u) + 32 * j < lim ? x_off + 64u * j : kOOB, 0, 0);
+        t.v[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, few_x_offset(l16, q16, j, lim, ldx2), 0, 0);
     };
     auto load_w = [&](W& t, int u, int cp) {
       const int k0 = u * UNIT, lim = u < u1 ? K - k0 : 0;
-      const uint32_t o0 = (int)(q16 * 8u) < lim ? w_off : kOOB, o1 = (int)(q16 * 8u) + 32 < lim ? w_off + 64u : kOOB;
 #pragma unroll
       for (int op = 0; op < NB; ++op) {
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(pw[op] + k0, lim > 0 ? (ncols - 1) * (int)ldb2 + lim * 2 : 0);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(pw[op] + k0, few_row_extent(ncols, lim, ldb2));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            t.v[op][i][j] = __builtin_amdgcn_raw_buffer_load_b128(rs, j ? o1 : o0, (4 * cp + i) * 16 * ldb2, 0);
+            t.v[op][i][j] = __builtin_amdgcn_raw_buffer_load_b128(rs, few_nk_offset(column[4 * cp + i], q16, j, lim), 0, 0);
       }
     };
     auto multiply = [&](const W& w, const X& x, auto cp_c) {
@@ -123,18 +125,19 @@ void ffn_few(FfnFew p) {
   } else {
     // A unit is two 32-deep steps; a lane's step is eight rows of eight columns.
     struct Step { u32x4_t w[NB][8], x; };
-    const uint32_t x_off = l16 * ldx2 + q16 * 16u;
-    const uint32_t w_off = (int)(l16 * 8u) < ncols ? 8u * q16 * ldb2 + l16 * 16u : kOOB;
+    uint32_t value[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) value[k] = few_kn_offset(l16, q16, k, ncols, ldb2);
     auto load = [&](Step& t, int u, int half) {
       const int k0 = u * UNIT + 32 * half, lim = u < u1 ? K - k0 : 0;      // past the split's end: zeros
-      const __amdgpu_buffer_rsrc_t xr = make_rsrc(px + k0, lim > 0 ? (mrows - 1) * (int)ldx2 + lim * 2 : 0);
-      t.x = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(q16 * 8u) < lim ? x_off : kOOB, 0, 0);
+      const __amdgpu_buffer_rsrc_t xr = make_rsrc(px + k0, few_row_extent(mrows, lim, ldx2));
+      t.x = __builtin_amdgcn_raw_buffer_load_b128(xr, few_x_offset(l16, q16, 0, lim, ldx2), 0, 0);
 #pragma unroll
       for (int op = 0; op < NB; ++op) {
         const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char*)pw[op] + (uint64_t)(uint32_t)k0 * ldb2,
-                                                    lim > 0 ? (min(lim, 32) - 1) * (int)ldb2 + ncols * 2 : 0);
+                                                    few_kn_extent(ncols, lim, ldb2));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t.w[op][k] = __builtin_amdgcn_raw_buffer_load_b128(wr, w_off, k * ldb2, kStream);
+        for (int k = 0; k < 8; ++k) t.w[op][k] = __builtin_amdgcn_raw_buffer_load_b128(wr, value[k], 0, kStream);
       }
     };
     auto multiply = [&](const Step& t) {
