@@ -3,7 +3,9 @@
 The gated feed-forward block with its backward pass (``GatedFFN``), the per-head norm of queries and
 keys with the position rotation and its gradient (``QKRotary``), the global gradient norm with
 clipping (``GradClip``).  ``lib`` holds the C functions of ``include/ge_block.h``; the classes own one handle and its zero-filled workspace, like
-``Plan``.  Argument marshalling only: every step of the computation runs in the HIP kernels.
+``Plan``.  A call may run on any stream of the plan's device; as with tensors used on a stream that is not their own, a plan is kept
+until its calls on other streams than the current one have run, and as long as a graph that holds them.
+Argument marshalling only: every step of the computation runs in the HIP kernels.
 The classes check shapes, strides, element types and devices of the tensors they are given; the
 library checks pointers and sizes again.
 """
@@ -137,13 +139,24 @@ class _Plan:
             _check(call(ctypes.byref(out)), where)
         self.handle = out.value
 
-    def _scratch(self, nbytes: int) -> torch.Tensor:
+    def _scratch(self, nbytes: int, stream: Optional[int] = None) -> torch.Tensor:
         """A zero-filled workspace that stays where it is as long as the plan lives (captured graphs
-        hold its address)."""
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the plan's workspace is made by its first call: call it once before the capture, "
-                               "or give the arguments a workspace")
-        return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        hold its address).  Taken and cleared on ``stream`` (a handle) where a call needs it, so that the
+        call finds it clear; without one on the device's current stream, and waited for: later
+        calls may run on any."""
+        if stream is None:
+            where = torch.cuda.device(self.device)
+        else:                                   # (an ExternalStream of handle 0 would be a stream of torch's pool)
+            where = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if stream
+                                      else torch.cuda.default_stream(self.device))
+        with where:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the plan's workspace is made by its first call: call it once before the capture, "
+                                   "or give the arguments a workspace")
+            workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            if stream is None:
+                torch.cuda.current_stream(self.device).synchronize()
+        return workspace
 
     def _stream(self, stream: Optional[int]) -> int:
         if stream is not None:
@@ -238,7 +251,7 @@ class GatedFFN(_Plan):
         _check(lib.ge_ffn_describe(self.handle, buf, len(buf)), "ge_ffn_describe")
         return buf.value.decode()
 
-    def _fit(self, args: Args, backward: bool) -> None:
+    def _fit(self, args: Args, backward: bool, stream: int) -> None:
         c, bf16 = self.desc, torch.bfloat16
         M, d, h = c.M, c.d, c.h
         kn = c.w_layout == GE_LAYOUT_KN
@@ -266,18 +279,19 @@ class GatedFFN(_Plan):
             if c.residual:
                 self._tensor(args, "residual", (M, d), bf16, (c.ldr, 1))
         if backward and args.tensors["workspace"] is None and self.workspace_backward is None:
-            self.workspace_backward = self._scratch(self.workspace_size(True))
+            self.workspace_backward = self._scratch(self.workspace_size(True), stream)
 
     def _run(self, args: Args, backward: bool, stream: Optional[int]) -> None:
+        stream = self._stream(stream)
         fits = args._fits.get(self, ())
         if backward not in fits:
-            self._fit(args, backward)
+            self._fit(args, backward, stream)
             args._fits[self] = (*fits, backward)
         if args.tensors["workspace"] is None:
             ws = self.workspace_backward if backward else self.workspace
             args.c.workspace, args.c.workspace_bytes = ws.data_ptr(), ws.numel()
         call = lib.ge_ffn_backward if backward else lib.ge_ffn_forward
-        st = call(self.handle, args._ref, self._stream(stream))
+        st = call(self.handle, args._ref, stream)
         if st != GE_OK:
             raise GemmEpilogueError(st, "ge_ffn_backward" if backward else "ge_ffn_forward")
 
@@ -369,7 +383,7 @@ class QKRotary(_Plan):
         self.workspace_bytes = n.value
         self.workspace = None        # made by the first backward
 
-    def _fit(self, args: Args, backward: bool) -> None:
+    def _fit(self, args: Args, backward: bool, stream: int) -> None:
         c = self.desc
         T, D = c.tokens, c.head_dim
         names = (("q", "k") if c.norm else ()) + ("dq_out", "dk_out", "dq", "dk") if backward else ("q", "k", "q_out", "k_out")
@@ -386,17 +400,18 @@ class QKRotary(_Plan):
                     if backward:
                         self._tensor(args, "dgain_" + s, (D,), torch.float32, (1,))
             if backward and args.tensors["workspace"] is None and self.workspace is None:
-                self.workspace = self._scratch(self.workspace_bytes)
+                self.workspace = self._scratch(self.workspace_bytes, stream)
 
     def _run(self, args: Args, backward: bool, stream: Optional[int]) -> None:
+        stream = self._stream(stream)
         fits = args._fits.get(self, ())
         if backward not in fits:
-            self._fit(args, backward)
+            self._fit(args, backward, stream)
             args._fits[self] = (*fits, backward)
         if backward and self.workspace is not None and args.tensors["workspace"] is None:
             args.c.workspace, args.c.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
         call = lib.ge_qk_backward if backward else lib.ge_qk_forward
-        st = call(self.handle, args._ref, self._stream(stream))
+        st = call(self.handle, args._ref, stream)
         if st != GE_OK:
             raise GemmEpilogueError(st, "ge_qk_backward" if backward else "ge_qk_forward")
 

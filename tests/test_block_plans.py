@@ -1,0 +1,127 @@
+"""Host logic of block.py's plans on the CPU, with stand-ins for the library and for torch's streams: on
+which stream a workspace is made, and what is refused before anything is launched."""
+from __future__ import annotations
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+import gemm_epilogue_transformer_tiled_amd as ge
+from gemm_epilogue_transformer_tiled_amd import block
+
+CURRENT, SIDE = 0x77, 0x1234
+BF16 = torch.bfloat16
+
+
+class World:
+    """What happened, in order, and the stream that was current."""
+
+    def __init__(self):
+        self.now, self.events, self.capturing = CURRENT, [], ()
+
+    @contextlib.contextmanager
+    def on(self, handle):
+        before, self.now = self.now, handle
+        try:
+            yield
+        finally:
+            self.now = before
+
+
+@pytest.fixture
+def world(monkeypatch):
+    w = World()
+
+    def create(*args):
+        return ge.GE_OK                    # (no handle: nothing for the real library to destroy)
+
+    def size(*args):
+        args[-1]._obj.value = 64
+        return ge.GE_OK
+
+    def call(name):
+        def f(handle, args, stream):
+            w.events.append((name, stream))
+            return ge.GE_OK
+        return f
+    lib = types.SimpleNamespace()
+    for name in block.EXPORTED:
+        kind = name.split("_", 2)[2]
+        setattr(lib, name, create if kind == "create" else size if kind == "workspace_size" else
+                (lambda handle: None) if kind == "destroy" else call(name))
+    monkeypatch.setattr(block, "lib", lib)
+    monkeypatch.setattr(block, "_raw_stream", lambda index: w.now)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda handle: w.on(handle))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: w.now in w.capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(
+        cuda_stream=w.now, synchronize=lambda: w.events.append(("waited", w.now))))
+    zeros = torch.zeros
+
+    def recorded(*args, **kw):
+        w.events.append(("cleared", w.now))
+        return zeros(*args, **kw)
+    monkeypatch.setattr(torch, "zeros", recorded)
+    return w
+
+
+def t(*shape, dtype=BF16):
+    return torch.ones(shape, dtype=dtype)
+
+
+def ffn_pack(**kw):
+    M, d, h = 4, 8, 16
+    base = dict(X=t(M, d), Wg=t(d, h), Wu=t(d, h), Wd=t(h, d), Y=t(M, d), G=t(M, h), U=t(M, h), dY=t(M, d), dX=t(M, d),
+                dWg=t(d, h), dWu=t(d, h), dWd=t(h, d))
+    return block.make_ffn_args(**{**base, **kw})
+
+
+def qk_pack(heads_q=2, heads_k=1, **kw):
+    T, D = 3, 8
+    base = dict(q=t(T, heads_q, D), k=t(T, heads_k, D), q_out=t(T, heads_q, D), k_out=t(T, heads_k, D),
+                positions=torch.arange(T), inv_freq=t(D // 2, dtype=torch.float32), gain_q=t(D), gain_k=t(D),
+                dq_out=t(T, heads_q, D), dk_out=t(T, heads_k, D), dq=t(T, heads_q, D), dk=t(T, heads_k, D),
+                dgain_q=t(D, dtype=torch.float32), dgain_k=t(D, dtype=torch.float32))
+    return block.make_qk_args(**{**base, **kw})
+
+
+def ffn():
+    return block.GatedFFN(4, 8, 16, device="cpu"), ffn_pack(), "ge_ffn_backward"
+
+
+def qk():
+    return block.QKRotary(3, 2, 1, 8, device="cpu"), qk_pack(), "ge_qk_backward"
+
+
+@pytest.mark.parametrize("make", [ffn, qk])
+@pytest.mark.parametrize("stream", [SIDE, 0, None])
+def test_a_workspace_made_by_a_call_is_cleared_on_its_stream(world, make, stream):
+    plan, args, name = make()
+    world.events.clear()
+    plan.backward(args, stream)
+    on = CURRENT if stream is None else stream
+    assert world.events == [("cleared", on), (name, on)]
+    world.events.clear()
+    plan.backward(args, stream)
+    assert world.events == [(name, on)]
+
+
+@pytest.mark.parametrize("make", [ffn, qk])
+def test_no_workspace_is_made_on_a_capturing_stream(world, make):
+    plan, args, _ = make()
+    world.capturing = (SIDE,)
+    with pytest.raises(RuntimeError):
+        plan.backward(args, SIDE)
+    plan.backward(args)                    # another stream's capture does not concern it
+    plan.backward(args, SIDE)              # made by now
+
+
+def test_a_plan_waits_for_the_workspace_it_is_made_with(world):
+    """The first call may be on any stream."""
+    block.GatedFFN(4, 8, 16, device="cpu")
+    block.GradClip([t(5)], device="cpu")
+    assert world.events == [("cleared", CURRENT), ("waited", CURRENT)] * 2
