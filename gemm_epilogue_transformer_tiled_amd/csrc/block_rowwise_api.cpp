@@ -127,8 +127,10 @@ bool fill(const ge_qk_plan* h, const ge_qk_args_t* a, bool backward, ge::QkParam
     in[n_in++] = Matrix{a->inv_freq, 1, d.rot_dim / 2, d.rot_dim / 2, 4};
   }
   if (backward && d.norm) {
-    for (float* g : {a->dgain_q, a->dgain_k}) {
-      if (!g && (g == a->dgain_q ? d.heads_q : d.heads_k) > 0) return false;
+    float* const dgain[2] = {a->dgain_q, a->dgain_k};
+    for (int w = 0; w < 2; ++w) {
+      float* const g = dgain[w];
+      if (!g && sides[w].heads > 0) return false;
       if (!g) continue;
       if (!aligned(g, 4)) return false;
       out[n_out++] = Matrix{g, 1, d.head_dim, d.head_dim, 4};
