@@ -183,6 +183,17 @@ class _Plan:
             if n > 1 and want is not None and have != want:
                 raise ValueError(f"{name} has strides {t.stride()}, the plan {tuple(strides)}")
 
+    def _workspace(self, args: Args) -> None:
+        """Raises ValueError unless the pack's workspace, if it has one, is dense memory of the plan's device
+        (its size and alignment are the library's to check)."""
+        w = args.tensors["workspace"]
+        if w is None:
+            return
+        if w.device != self.device:
+            raise ValueError(f"workspace is on {w.device}, the plan on {self.device}")
+        if not w.is_contiguous():
+            raise ValueError("workspace is not contiguous")
+
     def close(self) -> None:
         if self.handle:
             getattr(lib, self._destroy)(self.handle)
@@ -278,6 +289,7 @@ class GatedFFN(_Plan):
             self._tensor(args, "Y", (M, d), bf16, (c.ldy, 1))
             if c.residual:
                 self._tensor(args, "residual", (M, d), bf16, (c.ldr, 1))
+        self._workspace(args)
         if backward and args.tensors["workspace"] is None and self.workspace_backward is None:
             self.workspace_backward = self._scratch(self.workspace_size(True), stream)
 
@@ -399,6 +411,8 @@ class QKRotary(_Plan):
                     self._tensor(args, "gain_" + s, (D,), self.dtype, (1,))
                     if backward:
                         self._tensor(args, "dgain_" + s, (D,), torch.float32, (1,))
+            if backward:
+                self._workspace(args)
             if backward and args.tensors["workspace"] is None and self.workspace is None:
                 self.workspace = self._scratch(self.workspace_bytes, stream)
 
@@ -465,6 +479,7 @@ class GradClip(_Plan):
     def _fit(self, args: Args) -> None:
         if args.outs is None and args.tensors["norm"] is None:
             raise ValueError("neither a norm nor outputs to write")
+        self._workspace(args)
         if args.tensors["norm"] is not None:
             self._tensor(args, "norm", (1,), torch.float32)
         for kind in (args.grads, args.outs):

@@ -125,3 +125,29 @@ def test_a_plan_waits_for_the_workspace_it_is_made_with(world):
     block.GatedFFN(4, 8, 16, device="cpu")
     block.GradClip([t(5)], device="cpu")
     assert world.events == [("cleared", CURRENT), ("waited", CURRENT)] * 2
+
+
+def clip():
+    grads = [t(5)]
+    return block.GradClip(grads, device="cpu"), lambda **kw: block.make_clip_args(grads, grads, **kw), \
+        lambda plan, args: plan.run(args)
+
+
+WITH_WORKSPACE = {
+    "ffn forward": lambda: (ffn()[0], ffn_pack, lambda plan, args: plan.forward(args)),
+    "ffn backward": lambda: (ffn()[0], ffn_pack, lambda plan, args: plan.backward(args)),
+    "qk backward": lambda: (qk()[0], qk_pack, lambda plan, args: plan.backward(args)),
+    "clip": clip,
+}
+
+
+@pytest.mark.parametrize("which", list(WITH_WORKSPACE))
+def test_workspaces_of_another_device_or_not_dense_are_refused(world, which):
+    plan, pack, call = WITH_WORKSPACE[which]()
+    call(plan, pack(workspace=torch.empty(256, dtype=torch.uint8)))
+    world.events.clear()
+    for bad in (torch.empty(256, dtype=torch.uint8, device="meta"), torch.empty(512, dtype=torch.uint8)[::2],
+                torch.empty(1, dtype=torch.uint8).expand(256)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(plan, pack(workspace=bad))
+    assert world.events == []              # nothing was launched
