@@ -409,8 +409,8 @@ class QKRotary(_Plan):
             for s, heads in (("q", c.heads_q), ("k", c.heads_k)):
                 if heads:
                     self._tensor(args, "gain_" + s, (D,), self.dtype, (1,))
-                    if backward:
-                        self._tensor(args, "dgain_" + s, (D,), torch.float32, (1,))
+                if backward:                    # (written without heads too, where it is given)
+                    self._tensor(args, "dgain_" + s, (D,), torch.float32, (1,), optional=not heads)
             if backward:
                 self._workspace(args)
             if backward and args.tensors["workspace"] is None and self.workspace is None:

@@ -151,3 +151,16 @@ def test_workspaces_of_another_device_or_not_dense_are_refused(world, which):
         with pytest.raises(ValueError, match="workspace"):
             call(plan, pack(workspace=bad))
     assert world.events == []              # nothing was launched
+
+
+@pytest.mark.parametrize("heads_q,heads_k,name", [(2, 0, "dgain_k"), (0, 2, "dgain_q")])
+def test_gain_gradients_of_a_side_without_heads(world, heads_q, heads_k, name):
+    """They may be left out; one that is given is written (zeros), so it has to fit."""
+    plan = block.QKRotary(3, heads_q, heads_k, 8, device="cpu")
+    plan.backward(qk_pack(heads_q, heads_k, **{name: None}))
+    plan.backward(qk_pack(heads_q, heads_k))
+    world.events.clear()
+    for bad in (t(4, dtype=torch.float32), t(8), t(16, dtype=torch.float32)[::2], torch.empty(8, device="meta")):
+        with pytest.raises(ValueError, match=name):
+            plan.backward(qk_pack(heads_q, heads_k, **{name: bad}))
+    assert world.events == []
