@@ -14,6 +14,7 @@
 // The waves' sums meet in LDS in wave order, the workgroups' in the workspace in split order (the
 // last workgroup of a tile, found by a ticket, adds them up), so equal calls give equal bits.
 #include "ge_block_internal.h"
+#include "ge_ffn_act.h"
 #include "ge_ffn_few_addr.h"
 #include "ge_kernel_impl.h"
 
@@ -274,7 +275,7 @@ void ffn_few(FfnFew p) {
     if constexpr (PAIR) {
       f32x4_t h;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = activate<ACT>(v[0][i][e]) * v[NB - 1][i][e];
+      for (int e = 0; e < 4; ++e) h[e] = gate<ACT>(v[0][i][e]) * v[NB - 1][i][e];
       put(p.Y, p.ldy, row, h);
       if (p.Y2) {
         put(p.Y2, p.ldy2, row, v[0][i]);

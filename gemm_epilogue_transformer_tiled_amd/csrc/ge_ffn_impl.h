@@ -32,6 +32,7 @@
 // gradient 975 us (1.52), weight gradients 1,600-1,680 us (1.32-1.38); the gated gradient 670 us (1.10):
 // its epilogue moves 900 MB (G, U in; dG, dU, H out) that the loop does not hide.
 #include "ge_block_internal.h"
+#include "ge_ffn_act.h"
 #include "ge_kernel_impl.h"
 
 namespace ge {
@@ -84,7 +85,7 @@ __device__ __forceinline__ uint32_t swz_col(uint32_t k) {
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float z, float& a, float& s) {
   if constexpr (ACT == ACT_RELU) {
-    a = fmaxf(z, 0.0f);
+    a = relu_nan(z);
     s = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float c = z > 200.0f ? 200.0f : (z < -200.0f ? -200.0f : z), q = kGeluCubic * c * c;
@@ -572,7 +573,7 @@ void ffn_product(FfnLaunch l) {
     };
 #pragma unroll
     for (int j = 0; j < T::FM / 2; ++j) {
-      stage(j, [&](int i, int r, int e) { return activate<ACT>(acc[0][i][r][e]) * acc[NB - 1][i][r][e]; });
+      stage(j, [&](int i, int r, int e) { return gate<ACT>(acc[0][i][r][e]) * acc[NB - 1][i][r][e]; });
       write(j, y_rs, p.ldy);
       if (save) {
         stage(j, [&](int i, int r, int e) { return acc[0][i][r][e]; });

@@ -39,7 +39,8 @@ extern "C" {
  *             dX = dG Wg^T + dU Wu^T   dWg = X^T dG   dWu = X^T dU   dWd = H^T dY
  *
  * Activations: GE_ACT_NONE, GE_ACT_RELU (its derivative is 1 above zero, else 0),
- * GE_ACT_GELU_TANH, GE_ACT_SILU, with the formulas of gemm_epilogue.h.
+ * GE_ACT_GELU_TANH, GE_ACT_SILU, with the formulas of gemm_epilogue.h.  A NaN gate stays NaN with
+ * each of them.
  *
  * Numerics: products are summed in fp32.  Rounded to bf16, to nearest even: H before its product
  * with Wd, dG and dU (and, in the backward pass, H rebuilt from the given G and U) before theirs,
