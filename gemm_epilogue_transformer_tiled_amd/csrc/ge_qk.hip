@@ -314,10 +314,13 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
               p.pos64 ? (double)((const int64_t*)p.positions)[t0 + q] : (double)((const int32_t*)p.positions)[t0 + q];
           double turns_of = pos * (double)p.inv_freq[f] * 0.15915494309189533577;     // angle / 2 pi
           turns_of -= __builtin_rint(turns_of);
+          // the turn's rounding to fp32 (up to 9e-8 of angle, more than the sine's own error) is made good
+          // to first order
+          const float turn = (float)turns_of, rest = (float)(turns_of - (double)turn) * 6.283185307f;
           float s, c;
-          sincospif(2.0f * (float)turns_of, &s, &c);
-          turn_c[i] = c * p.amplitude;
-          turn_s[i] = s * p.amplitude;
+          sincospif(2.0f * turn, &s, &c);
+          turn_c[i] = fmaf(-s, rest, c) * p.amplitude;
+          turn_s[i] = fmaf(c, rest, s) * p.amplitude;
         }
         __syncthreads();
       }
