@@ -163,6 +163,16 @@ __device__ __forceinline__ float group_sum(float v, int G) {
   return v;
 }
 
+// 1 / sqrt(mean square + eps).  The hardware's takes a subnormal argument for zero; one is met only where
+// eps itself is below the normal range (uniform): then small ones are scaled by 2^64 first.
+__device__ __forceinline__ float inv_rms(float ss, float inv_d, float eps) {
+  const float m = fmaf(ss, inv_d, eps);
+  if (eps >= 0x1p-126f) return __builtin_amdgcn_rsqf(m);
+  const bool tiny = m < 0x1p-64f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? m * 0x1p64f : m);
+  return tiny ? r * 0x1p32f : r;
+}
+
 // Element offset of a head within a turn's tokens.  WIDE: 24-bit factors, 31-bit products (checked
 // on the host), so the addresses take two full-rate multiplies.
 template <bool WIDE>
@@ -258,7 +268,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) ss = fmaf(x.a[j], x.a[j], fmaf(x.b[j], x.b[j], ss));
-            const float r = __builtin_amdgcn_rsqf(fmaf(group_sum(ss, G), inv_d, p.eps));
+            const float r = inv_rms(group_sum(ss, G), inv_d, p.eps);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               x.a[j] = x.a[j] * r * gain[w].a[j];
@@ -290,7 +300,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_rotary(QkParams p) {
             }
             ss = group_sum(ss, G);
             ex = group_sum(ex, G);
-            const float r = __builtin_amdgcn_rsqf(fmaf(ss, inv_d, p.eps));
+            const float r = inv_rms(ss, inv_d, p.eps);
             const float mean = ex * r * inv_d;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

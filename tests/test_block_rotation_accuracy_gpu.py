@@ -44,3 +44,36 @@ def test_angles_are_not_rounded_to_a_fp32_turn():
     assert float(excess.abs().max()) <= 2.0 ** -21
     assert float(d.abs().mean()) > 2e-8
     assert abs(float((excess * d.sign()).mean())) <= 6 * 2.0 ** -21 / math.sqrt(n)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("x", [1e-17, 1e-18, 1e-19, 1e-20, 1e-21])
+@pytest.mark.parametrize("eps", [0.0, 1e-42])
+def test_norm_of_very_small_heads(x, eps, dtype):
+    """Without an eps to speak of, heads whose mean square is subnormal are normalised all the same.  Results
+    below 2^-126 are multiples of 2^-149, a unit: the D products are each off by half of one, sums of multiples are exact, so
+    the mean is off by half a unit from them, half from its own rounding and half from eps's: less than 2, and
+    its root by 1 / mean units relative.  Everything else is off by a few 2^-24."""
+    D = 64
+    q = torch.full((3, 2, D), x, device="cuda", dtype=dtype)
+    q[:, :, 1::2] *= -1
+    q[1] *= 2
+    out, dq = torch.empty_like(q), torch.empty_like(q)
+    gain = torch.ones(D, device="cuda", dtype=dtype)
+    plan = block.QKRotary(3, 2, 0, D, rot_dim=0, eps=eps, dtype=dtype)
+    plan.forward(block.make_qk_args(q=q, q_out=out, gain_q=gain))
+    v = q.double()
+    mean = v.square().mean(-1, keepdim=True) + eps
+    want = v / mean.sqrt()
+    unit = 2.0 ** -149
+    loss = unit / mean + 16 * 2.0 ** -24 + torch.finfo(dtype).eps / 2
+    assert bool(((out.double() - want).abs() <= want.abs() * loss).all()), (float(out[0, 0, 0]), float(want[0, 0, 0]))
+    dout = torch.zeros_like(q)
+    dout[..., 0] = 1.0
+    dgain = torch.empty(D, device="cuda")
+    plan.backward(block.make_qk_args(q=q, gain_q=gain, dq_out=dout, dq=dq, dgain_q=dgain))
+    n, r = want, 1 / mean.sqrt()
+    e = dout.double()
+    size = r * (e.abs() + n.abs() * (e * n).abs().mean(-1, keepdim=True))
+    assert bool(((dq.double() - r * (e - n * (e * n).mean(-1, keepdim=True))).abs() <= size * (3 * loss)).all())
+    assert dgain.isfinite().all()
