@@ -36,10 +36,8 @@ constexpr int64_t kMaxLd = int64_t(1) << 22;
 // (4096 x 11008, one row: 53 us against 68 in tiles, 16 rows 58 against 70; 2048 x 5632: 23 against 29;
 // 1024 x 2816: equal; 256 x 512: 10-14 against 10, and with 24 rows the tiles win or are even).
 constexpr int64_t kFewWeights = int64_t(8) << 20;
-// A tile's contraction is split over at most this many workgroups, and only in launches of at most
-// this many in all (three on every compute unit).
+// A tile's contraction is split over at most this many workgroups.
 constexpr int kMaxSplits = 16;
-constexpr int kMaxSplitGroups = 768;
 
 // Whether a launch's threads can be counted in 32 bits, which the runtime asks for.
 bool grid_fits(int tile, int64_t M, int64_t N, bool pair, int products) {
@@ -69,7 +67,7 @@ Choice pick(int mode, int64_t M, int64_t N, int64_t K, int products, int32_t ask
     const int bn = pair ? ti.bn_pair : ti.bn;
     const double tiles = (double)ceil_div(M, ti.bm) * (double)ceil_div(N, bn) * products;
     for (int s = 1; s <= (t == ge::FFN_T256 ? 1 : kMaxSplits); s *= 2) {
-      if (s > 1 && (slots < 4 * s || tiles * s > kMaxSplitGroups)) break;
+      if (s > 1 && (slots < 4 * s || tiles * s > ge::kFfnMaxSplitGroups)) break;
       // (workgroups of many rounds no longer end together)
       const double ratio = tiles * s / 256.0, rounds = ratio < 4.0 ? std::ceil(ratio) : ratio;
       const double mine = (double)ceil_div(slots, s);
@@ -99,8 +97,8 @@ bool add(ge::FfnLaunch& l, ge::FfnProduct p, const Choice& c, bool pair) {
   return true;
 }
 
-// Few rows: how a product is split.  One workgroup of eight waves on every compute unit at most, and
-// no more splits than the longest wave's share needs.
+// Few rows: how a product is split.  One workgroup of eight waves on every compute unit at most (so a
+// split launch has no more than 256), and no more splits than the longest wave's share needs.
 struct FewPlan { int tiles, splits; };
 FewPlan few_plan(int64_t N, int64_t K) {
   FewPlan f;
@@ -111,7 +109,6 @@ FewPlan few_plan(int64_t N, int64_t K) {
   f.splits = (int)std::max<int64_t>(1, ceil_div(units, waves * share));
   return f;
 }
-size_t few_ctr_bytes(const FewPlan& f) { return (size_t)f.tiles * ge::kFfnCtrStride * 4; }
 size_t few_part_bytes(const FewPlan& f, int operands) {
   return f.splits > 1 ? (size_t)f.tiles * f.splits * operands * ge::kFfnFewRows * ge::kFfnFewCols * 4 : 0;
 }
@@ -120,17 +117,12 @@ size_t hidden_bytes(const ge_ffn_desc_t& d) { return (size_t)d.M * (size_t)d.h *
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Workspace of both calls: [tickets][partial sums][H], or [tickets][partial sums][dG][dU][H].  The
-// tickets come first and take the same room in both, so one workspace may serve both in turn; the
-// launches of a call follow each other and use the tickets and the partial sums in turn.
+// tickets come first and take the same room in every workspace; the launches of a call follow each
+// other and use the tickets and the partial sums in turn.
 struct Layout { size_t part, hidden, total; };
 bool few_rows(const ge_ffn_desc_t& d) { return d.tile == 0 && d.M <= ge::kFfnFewRows && d.d * d.h >= kFewWeights; }
 FewPlan few_up(const ge_ffn_desc_t& d) { return few_plan(d.h, d.d); }
 FewPlan few_down(const ge_ffn_desc_t& d) { return few_plan(d.d, d.h); }
-size_t ticket_bytes(const ge_ffn_desc_t& d) {
-  size_t b = (size_t)kMaxSplitGroups * ge::kFfnCtrStride * 4;
-  if (few_rows(d)) b = std::max({b, few_ctr_bytes(few_up(d)), few_ctr_bytes(few_down(d))});
-  return round256(b);
-}
 size_t part_bytes(const Choice& c, int64_t M, int64_t N, bool pair, int products = 1) {
   if (c.splits < 2) return 0;
   const ge::FfnTileInfo ti = ge::ffn_tile_info(c.tile);
@@ -140,7 +132,7 @@ size_t part_bytes(const Choice& c, int64_t M, int64_t N, bool pair, int products
 Layout forward_layout(const ge_ffn_plan* p) {
   const ge_ffn_desc_t& d = p->desc;
   Layout l{};
-  l.part = ticket_bytes(d);
+  l.part = ge::kTicketBytes;
   const size_t sums = few_rows(d) ? std::max(few_part_bytes(few_up(d), 2), few_part_bytes(few_down(d), 1))
                                   : std::max(part_bytes(p->pair, d.M, d.h, true), part_bytes(p->down, d.M, d.d, false));
   l.hidden = l.part + round256(sums);
@@ -150,7 +142,7 @@ Layout forward_layout(const ge_ffn_plan* p) {
 Layout backward_layout(const ge_ffn_plan* p) {
   const ge_ffn_desc_t& d = p->desc;
   Layout l{};
-  l.part = ticket_bytes(d);
+  l.part = ge::kTicketBytes;
   l.hidden = l.part + round256(std::max({part_bytes(p->grad, d.M, d.h, false), part_bytes(p->dx, d.M, d.d, false),
                                          part_bytes(p->dw, d.d, d.h, false, 3)}));
   l.total = l.hidden + 3 * round256(hidden_bytes(d));

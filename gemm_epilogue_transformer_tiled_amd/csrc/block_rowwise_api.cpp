@@ -63,8 +63,9 @@ bool wide(const ge_qk_desc_t& d, const void* const* ptrs, int n_ptrs, const int6
   return true;
 }
 
+// [tickets' room, unused][partial gain gradients]
 size_t gain_bytes(const ge_qk_plan* h) {
-  return h->desc.norm ? (size_t)std::max(h->grid_backward, 1) * 2 * (size_t)h->desc.head_dim * 4 : 0;
+  return h->desc.norm ? ge::kTicketBytes + (size_t)std::max(h->grid_backward, 1) * 2 * (size_t)h->desc.head_dim * 4 : 0;
 }
 
 struct Side {           // q or k
@@ -147,7 +148,7 @@ bool fill(const ge_qk_plan* h, const ge_qk_args_t* a, bool backward, ge::QkParam
   }
   p.positions = a->positions;
   p.inv_freq = a->inv_freq;
-  p.part = static_cast<float*>(a->workspace);
+  if (backward && d.norm) p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a->workspace) + ge::kTicketBytes);
   p.tokens = d.tokens;
   p.turns = h->turns;
   p.head_dim = d.head_dim;
@@ -286,6 +287,9 @@ struct ge_clip_plan {
 
 namespace {
 
+// [tickets' room, unused][partial sums]
+constexpr size_t kClipBytes = ge::kTicketBytes + ge::kClipPartials * sizeof(double);
+
 int64_t clip_launches(const ge_clip_plan* h) { return ceil_div(h->live, ge::kClipTensors); }
 
 struct Range {
@@ -341,7 +345,7 @@ void ge_clip_destroy(ge_clip_handle_t h) {
 
 ge_status_t ge_clip_workspace_size(ge_clip_handle_t h, size_t* bytes) {
   if (!h || !bytes) return GE_ERR_INVALID_ARG;
-  *bytes = ge::kClipPartials * sizeof(double);
+  *bytes = kClipBytes;
   return GE_OK;
 }
 
@@ -351,7 +355,7 @@ ge_status_t ge_clip_run(ge_clip_handle_t h, const ge_clip_args_t* a, void* strea
   if (h->n > 0 && !a->in) return GE_ERR_INVALID_ARG;
   if (!a->out && !a->norm) return GE_ERR_INVALID_ARG;
   if (a->norm && !aligned(a->norm, 4)) return GE_ERR_INVALID_ARG;
-  const size_t ws = ge::kClipPartials * sizeof(double);
+  const size_t ws = kClipBytes;
   if (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < ws) return GE_ERR_INVALID_ARG;
   // outputs (and the norm and the workspace) overlap nothing but their own input, exactly
   {
@@ -384,7 +388,7 @@ ge_status_t ge_clip_run(ge_clip_handle_t h, const ge_clip_args_t* a, void* strea
   if (!ge::block::is_current(h->device)) return GE_ERR_DEVICE;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
-  double* part = static_cast<double*>(a->workspace);
+  double* part = reinterpret_cast<double*>(static_cast<unsigned char*>(a->workspace) + ge::kTicketBytes);
   const int64_t launches = clip_launches(h);
   const int most = launches > 0 ? (int)(ge::kClipPartials / launches) : 0;   // workgroups of one norm launch
   // pass 0: partial sums of every launch's tensors; pass 1: the norm and the scaled values

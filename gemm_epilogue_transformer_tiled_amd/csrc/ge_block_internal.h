@@ -34,6 +34,12 @@ struct FfnLaunch {
   uint32_t* ctr;              // splits > 1: tickets per tile, zero between calls
 };
 constexpr uint32_t kFfnCtrStride = 16;       // 64 bytes between tickets
+// A contraction is split only in launches of at most this many workgroups (three on every compute unit).
+constexpr int kFfnMaxSplitGroups = 768;
+// Every operator's workspace begins with the room of the most tickets and keeps its data behind it: a
+// workspace may serve calls of several handles in turn, and what one leaves is never another's ticket.
+constexpr size_t kTicketBytes = (size_t)kFfnMaxSplitGroups * kFfnCtrStride * 4;
+static_assert(kTicketBytes % 256 == 0, "data behind the tickets is aligned");
 
 struct FfnTileInfo { int bm, bn, bn_pair; };
 inline FfnTileInfo ffn_tile_info(int tile) {

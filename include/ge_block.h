@@ -15,9 +15,10 @@
  *
  * Workspace: device scratch of the size *_workspace_size reports, 16-byte aligned, owned by the
  * caller, ZERO-FILLED before its first use; each call that completes leaves its counters at zero
- * again.  HAZARD: calls that share a workspace must not overlap in time (two streams, or two
- * graphs replayed at once); give concurrent calls workspaces of their own, and clear a workspace
- * again after a call that did not complete.
+ * again.  One workspace of the largest size may serve handles of all operators of this header in
+ * turn; where anything else wrote to it, it is cleared again.  HAZARD: calls that share a workspace
+ * must not overlap in time (two streams, or two graphs replayed at once); give concurrent calls
+ * workspaces of their own, and clear a workspace again after a call that did not complete.
  *
  * Errors: every call returns a status, nothing is enqueued unless it is GE_OK (GE_ERR_HIP: a
  * launch failed, and earlier launches of the same call may have run), nothing aborts.
@@ -166,7 +167,8 @@ typedef struct ge_qk_plan* ge_qk_handle_t;
 ge_status_t ge_qk_validate(const ge_qk_desc_t* desc);
 ge_status_t ge_qk_create(const ge_qk_desc_t* desc, ge_qk_handle_t* out);
 /* Workspace bytes of ge_qk_backward (partial sums of the gains' gradients, every one written by
- * each call: it needs no zero fill); 0 without norm.  ge_qk_forward needs none. */
+ * each call: one that no other operator uses needs no zero fill); 0 without norm.  ge_qk_forward
+ * needs none. */
 ge_status_t ge_qk_workspace_size(ge_qk_handle_t handle, size_t* bytes);
 /* One launch. */
 ge_status_t ge_qk_forward(ge_qk_handle_t handle, const ge_qk_args_t* args, void* stream);
@@ -194,7 +196,7 @@ typedef struct {
   const void* const* in;              /* host array of n device pointers, read during the call */
   void* const* out;                   /* host array of n device pointers; NULL: only the norm */
   float* norm;                        /* device, one float; may be NULL with out */
-  void* workspace;                    /* needs no zero fill */
+  void* workspace;                    /* (one that no other operator uses needs no zero fill) */
   size_t workspace_bytes;
   float max_norm;                     /* >= 0 (may be infinite) */
   float eps;                          /* finite, >= 0 */

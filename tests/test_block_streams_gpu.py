@@ -95,3 +95,63 @@ def test_plans_made_behind_a_busy_stream_are_ready_on_another():
         torch.cuda.synchronize()
         runs.append((Y, norm))
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_one_workspace_for_all_operators_in_turn():
+    """Calls of several plans share one workspace, eagerly and in a graph: what one leaves there is never
+    another's ticket."""
+    gen = torch.Generator("cuda").manual_seed(4)
+    sizes = [(64, 264, 4104), (9, 2048, 4104), (333, 520, 1032)]
+    ffns, runs = [], []
+    for M, d, h in sizes:
+        c = dict(X=normal(gen, M, d), Wg=normal(gen, d, h, std=d ** -0.5), Wu=normal(gen, d, h, std=d ** -0.5),
+                 Wd=normal(gen, h, d, std=h ** -0.5), dY=normal(gen, M, d, std=0.1))
+        ffns.append((block.GatedFFN(M, d, h, save=True), c))
+    T, hq, hk, D = 3000, 8, 2, 64
+    qk = block.QKRotary(T, hq, hk, D)
+    q, k = normal(gen, T, hq, D), normal(gen, T, hk, D)
+    heads = dict(q=q, k=k, dq_out=normal(gen, T, hq, D), dk_out=normal(gen, T, hk, D), gain_q=normal(gen, D), gain_k=normal(gen, D),
+                 positions=torch.arange(T, device="cuda"), inv_freq=block.rotary_frequencies(D)[0].cuda())
+    grads = [normal(gen, 100_000), normal(gen, 3_000_000)]
+    clip = block.GradClip(grads)
+    e = torch.empty_like
+    for shared in (False, True):
+        size = max(p.workspace_size(b) for p, _ in ffns for b in (False, True))
+        size = max(size, qk.workspace_bytes, clip.workspace.numel())
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda") if shared else None
+        outs, calls = [], []
+        for plan, c in ffns:
+            M, h = c["X"].shape[0], c["Wg"].shape[1]
+            o = dict(Y=e(c["X"]), G=c["X"].new_empty(M, h), U=c["X"].new_empty(M, h), dX=e(c["X"]), dWg=e(c["Wg"]),
+                     dWu=e(c["Wu"]), dWd=e(c["Wd"]))
+            args = block.make_ffn_args(**c, **o, workspace=ws)
+            outs += o.values()
+            calls += [lambda p=plan, a=args: p.forward(a), lambda p=plan, a=args: p.backward(a)]
+        o = dict(dq=e(q), dk=e(k), dgain_q=torch.empty(D, device="cuda"), dgain_k=torch.empty(D, device="cuda"))
+        qa = block.make_qk_args(**heads, **o, workspace=ws)
+        clipped, norm = [e(g) for g in grads], torch.empty(1, device="cuda")
+        ca = block.make_clip_args(grads, clipped, norm=norm, workspace=ws)
+        outs += [*o.values(), *clipped, norm]
+        others = [lambda: qk.backward(qa), lambda: clip.run(ca)]
+
+        def step():
+            for call in calls:
+                call()
+                for other in others:
+                    other()
+        step()
+        torch.cuda.synchronize()
+        runs.append([t.clone() for t in outs])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for _ in range(2):
+            for t in outs:
+                t.fill_(float("nan"))
+            graph.replay()
+            step() if shared else None
+            torch.cuda.synchronize()
+            runs.append([t.clone() for t in outs])
+    for run in runs[1:]:
+        for a, b in zip(runs[0], run):
+            assert torch.equal(a, b)
