@@ -358,13 +358,23 @@ def make_qk_args(q=None, k=None, q_out=None, k_out=None, positions=None, inv_fre
     return a
 
 
+def _apart(tokens: int, heads: int, head_dim: int, strides: Sequence[int]) -> bool:
+    """Whether (token, head) strides keep the heads of all tokens apart, as outputs' strides have to."""
+    rows = [(s, n) for s, n in zip(strides, (tokens, heads)) if n != 1]
+    if 0 in (tokens, heads) or not rows:
+        return True
+    (low, n), (high, _) = min(rows), max(rows)
+    return low >= head_dim and (len(rows) < 2 or high >= (n - 1) * low + head_dim)
+
+
 class QKRotary(_Plan):
     """Per-head RMS norm of queries and keys with the position rotation, and its gradient.
 
     ``forward`` reads q, k, positions, inv_freq (and the gains), writes q_out, k_out (which may be q and
     k); ``backward`` reads dq_out, dk_out (and, with the norm, q, k and the gains), writes dq, dk and, with
     the norm, dgain_q, dgain_k.  ``*_strides``: (token, head) strides in elements, default packed; the
-    gradients of the outputs have the outputs' strides, dq and dk those of q and k unless given."""
+    gradients of the outputs have the outputs' strides, dq and dk those of q and k unless given, or packed
+    where q and k repeat elements (an expanded tensor)."""
 
     _destroy = "ge_qk_destroy"
 
@@ -384,7 +394,8 @@ class QKRotary(_Plan):
         k = tuple(k_strides or (heads_k * head_dim, head_dim))
         oq = tuple(q_out_strides or (heads_q * head_dim, head_dim))
         ok = tuple(k_out_strides or (heads_k * head_dim, head_dim))
-        dq, dk = tuple(dq_strides or q), tuple(dk_strides or k)
+        own = lambda s, heads: s if _apart(tokens, heads, head_dim, s) else (heads * head_dim, head_dim)  # noqa: E731
+        dq, dk = tuple(dq_strides or own(q, heads_q)), tuple(dk_strides or own(k, heads_k))
         self.strides = dict(q=q, k=k, q_out=oq, k_out=ok, dq_out=oq, dk_out=ok, dq=dq, dk=dk)
         self.desc = ge_qk_desc_t(tokens, heads_q, heads_k, *q, *k, *oq, *ok, *dq, *dk, head_dim,
                                  head_dim if rot_dim is None else rot_dim, PAIR_NAMES[pairs], int(norm), DTYPES[dtype],

@@ -164,3 +164,20 @@ def test_gain_gradients_of_a_side_without_heads(world, heads_q, heads_k, name):
         with pytest.raises(ValueError, match=name):
             plan.backward(qk_pack(heads_q, heads_k, **{name: bad}))
     assert world.events == []
+
+
+@pytest.mark.parametrize("q_strides", [(0, 0), (0, 8), (8, 0), (16, 4)])
+def test_repeated_inputs_have_packed_gradients(world, q_strides):
+    """Inputs may repeat, their gradients may not: unless strides are given for these, they are packed."""
+    plan = block.QKRotary(3, 2, 1, 8, q_strides=q_strides, device="cpu")
+    d = plan.desc
+    assert (d.q_token, d.q_head) == q_strides and (d.dq_token, d.dq_head) == (16, 8)
+    assert plan.strides["dq"] == (16, 8) and plan.strides["dk"] == (8, 8)
+
+
+def test_gradients_follow_inputs_that_keep_heads_apart(world):
+    for strides in ((16, 8), (64, 8), (8, 24), (64, 16)):
+        plan = block.QKRotary(3, 2, 1, 8, q_strides=strides, device="cpu")
+        assert (plan.desc.dq_token, plan.desc.dq_head) == strides
+    one = block.QKRotary(1, 2, 1, 8, q_strides=(0, 8), device="cpu")          # one token: its stride does not matter
+    assert one.strides["dq"] == (0, 8)
