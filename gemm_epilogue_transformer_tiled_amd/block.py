@@ -328,6 +328,10 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
         raise ValueError("rot_dim is even and not negative")
     if not (factor >= 1.0 and math.isfinite(factor)):
         raise ValueError("factor is at least 1")
+    if not (base > 0.0 and math.isfinite(base)):
+        raise ValueError("base is above 0 and finite")
+    if scaling == "by_parts" and not (slow <= fast and original_length > 0):
+        raise ValueError("slow is at most fast, original_length above 0")
     i = torch.arange(rot_dim // 2, dtype=torch.float64)
     if scaling == "base":
         base = base * factor ** (rot_dim / (rot_dim - 2)) if rot_dim > 2 else base
@@ -337,7 +341,7 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
         f = f / factor
     elif scaling == "by_parts":
         turns = original_length * f / (2 * math.pi)
-        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0) if slow < fast else (turns >= slow).double()
         f = f * keep + f / factor * (1.0 - keep)
         amplitude = 0.1 * math.log(factor) + 1.0
     elif scaling not in ("none", "base"):

@@ -3,6 +3,7 @@ which stream a workspace is made, and what is refused before anything is launche
 from __future__ import annotations
 
 import contextlib
+import math
 import types
 
 import pytest
@@ -181,3 +182,22 @@ def test_gradients_follow_inputs_that_keep_heads_apart(world):
         assert (plan.desc.dq_token, plan.desc.dq_head) == strides
     one = block.QKRotary(1, 2, 1, 8, q_strides=(0, 8), device="cpu")          # one token: its stride does not matter
     assert one.strides["dq"] == (0, 8)
+
+
+def test_frequencies_blended_over_no_range():
+    """With slow = fast nothing is blended: what makes fewer turns is divided, what makes as many is kept."""
+    plain, _ = block.rotary_frequencies(64)
+    turns = 4096 * plain.double() / (2 * math.pi)
+    for border in (1.0, 7.5, 4096 / (2 * math.pi)):             # (the last: the first frequency's own)
+        got, _ = block.rotary_frequencies(64, scaling="by_parts", factor=4.0, slow=border, fast=border)
+        kept = turns > border * (1 + 1e-6)
+        divided = turns < border * (1 - 1e-6)
+        assert torch.equal(got[kept], plain[kept]) and torch.equal(got[divided], plain[divided] / 4)
+        assert got.isfinite().all()
+
+
+@pytest.mark.parametrize("bad", [dict(slow=2.0, fast=1.0), dict(slow=math.nan), dict(original_length=0), dict(base=0.0),
+                                 dict(base=-1.0), dict(base=math.inf), dict(base=math.nan)])
+def test_frequencies_refused(bad):
+    with pytest.raises(ValueError):
+        block.rotary_frequencies(64, scaling="by_parts", factor=4.0, **bad)
