@@ -109,7 +109,8 @@ def _check(status: int, where: str) -> None:
 
 class Args:
     """A pack of device pointers (``.c``, the C struct) and the tensors behind them, which it
-    keeps alive.  Build it once and pass it to every call on those tensors."""
+    keeps alive, with the plans it was used with and their workspaces.  Build it once and pass it to every
+    call on those tensors."""
 
     def __init__(self, struct: ctypes.Structure, tensors: Dict[str, Optional[torch.Tensor]]):
         self.c = struct

@@ -27,6 +27,7 @@ struct ge_qk_plan {
 namespace {
 
 constexpr int kMostTokens = 16;          // of one turn
+static_assert(ge::kQkMaxAngles >= ge::kQkThreads, "a turn's angles: about one a thread, or one token's (up to 256)");
 constexpr int64_t kMaxTokens = int64_t(1) << 40, kMaxHeads = int64_t(1) << 20, kMaxStride = int64_t(1) << 40;
 
 // Heads of tokens as rows of elements: the larger stride separates rows.  Exact for the layouts

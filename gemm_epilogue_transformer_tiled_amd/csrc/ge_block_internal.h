@@ -93,7 +93,7 @@ struct QkKind { bool bf16, wide, half, norm, backward; };
 hipError_t launch_qk(const QkKind& kind, const QkParams& p, hipStream_t s);
 hipError_t launch_qk_gains(const float* part, int rows, int head_dim, float* dgain_q, float* dgain_k, hipStream_t s);
 constexpr int kQkThreads = 256;
-constexpr int kQkMaxAngles = 1024;      // angles of one turn kept in LDS (8 KB)
+constexpr int kQkMaxAngles = 256;       // angles of one turn kept in LDS (2 KB): at most one a thread
 constexpr int kQkMaxBackwardGrid = 1024;
 
 // ---- gradient norm and clipping ----

@@ -258,7 +258,7 @@ void ffn_product(FfnLaunch l) {
     const bool in_k = (int)(r_x * 8u) < b_lim;
 #pragma unroll
     for (int t = 0; t < LBF; ++t) {
-      const uint32_t g = (uint32_t)(wave * LBF + t), u = g % (uint32_t)B_UNITS;   // wave-uniform
+      const uint32_t g = (uint32_t)(wave * LBF + t);   // wave-uniform
       uint32_t off = b_voff[t];
       if constexpr (MASK) off = in_k ? off : kOOB;
       if (PAIR && g >= (uint32_t)B_UNITS)
