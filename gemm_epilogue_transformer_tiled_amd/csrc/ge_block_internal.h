@@ -13,7 +13,8 @@ enum FfnMode : int {
   FFN_GRAD = 2,   // t = A B: Y = t * E2 * act'(E1) (dG), Y2 = t * act(E1) (dU), Y3 = act(E1) * E2 (H)
   FFN_DUAL = 3,   // Y = A B + A2 B2
   FFN_WGRAD = 4,  // Y = A B with both operands given contraction-major: A [K][M], B [K][N]
-  FFN_MODES = 5
+  FFN_MODES = 5,
+  FFN_I8 = 5      // not of the block: codes, on the same mainloop (ge_i8.hip)
 };
 enum FfnTile : int { FFN_T256 = 0, FFN_T128 = 1, FFN_T64 = 2, FFN_TILES = 3 };
 
@@ -32,6 +33,16 @@ struct FfnLaunch {
   int32_t splits;             // workgroups that share a tile's contraction (1 with the 256-row tiles)
   float* part;                // splits > 1: partial sums [tile][split][bm * bn * operands]
   uint32_t* ctr;              // splits > 1: tickets per tile, zero between calls
+};
+// What the product of codes adds: Y, E1 (residual) and bias bf16, or fp32 with `wide`.
+struct I8Epilogue {
+  const float *x_scale, *w_scale;
+  const void* bias;           // NULL: none
+  int32_t act;
+  bool wide;
+};
+struct I8Launch : FfnLaunch {
+  I8Epilogue ep;
 };
 constexpr uint32_t kFfnCtrStride = 16;       // 64 bytes between tickets
 // A contraction is split only in launches of at most this many workgroups (three on every compute unit).

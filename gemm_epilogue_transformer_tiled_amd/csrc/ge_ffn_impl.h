@@ -8,6 +8,8 @@
 //   GRAD   dH = dY Wd^T stays in registers; the epilogue reads G and U and writes dG, dU and H
 //   DUAL   dX = dG Wg^T + dU Wu^T: one accumulator, the contraction runs over both products
 //   WGRAD  dWg = X^T dG, dWu = X^T dU, dWd = H^T dY: one launch, both operands contraction-major
+// and a sixth, of int8 codes (I8, ge_i8.hip): rows of codes are staged and read like rows of half as many
+// bf16 values, the matrix core multiplies 64 codes where it multiplies 32 values, into int32 sums.
 //
 // Operand forms.  "Row" operands have the contraction contiguous ([rows][K]); they are staged as
 // [rows][64] with 128-byte rows and read as fragments by plain 16-byte LDS reads.  "Column"
@@ -37,6 +39,8 @@
 
 namespace ge {
 namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 template <int BM_, int BN_, int NB_, int WAVES_, int NSLOT_, bool PP_ = false>
 struct FTile {
@@ -102,10 +106,12 @@ __device__ __forceinline__ void act_and_slope(float z, float& a, float& s) {
   }
 }
 
-template <class T, int MODE, int ACT, bool AC, bool BC>
+// LAUNCH: FfnLaunch, or what a mode adds to it.
+template <class T, int MODE, int ACT, bool AC, bool BC, class LAUNCH = FfnLaunch>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(T::PP ? 2 : 1, T::PP ? 2 : 8)))
-void ffn_product(FfnLaunch l) {
-  constexpr bool PAIR = MODE == FFN_PAIR, DUAL = MODE == FFN_DUAL;
+void ffn_product(LAUNCH l) {
+  constexpr bool PAIR = MODE == FFN_PAIR, DUAL = MODE == FFN_DUAL, I8 = MODE == FFN_I8;
+  static_assert(!I8 || (!AC && !BC), "codes lie along the contraction");
   constexpr int NB = T::NB;
   static_assert((NB == 2) == PAIR, "two B operands: the gate/up pair");
   constexpr int BST = T::B_SLOT / 2;                   // 32-deep stage of B (two-wave loop, column B)
@@ -327,21 +333,27 @@ void ffn_product(FfnLaunch l) {
       }
   };
   // block (i, j): lane holds row 16 j + lane % 16, columns 16 i + 4 (lane / 16) .. +3
-  f32x4_t acc[NB][T::FN][T::FM];
+  using Acc = std::conditional_t<I8, i32x4_t, f32x4_t>;
+  Acc acc[NB][T::FN][T::FM];
 #pragma unroll
   for (int op = 0; op < NB; ++op)
 #pragma unroll
     for (int i = 0; i < T::FN; ++i)
 #pragma unroll
-      for (int j = 0; j < T::FM; ++j) acc[op][i][j] = f32x4_t{};
+      for (int j = 0; j < T::FM; ++j) acc[op][i][j] = Acc{};
   auto mfmas = [&](const Frags& f) {
 #pragma unroll
     for (int i = 0; i < T::FN; ++i)
 #pragma unroll
       for (int j = 0; j < T::FM; ++j)
 #pragma unroll
-        for (int op = 0; op < NB; ++op)
-          acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[op][i], f.a[j], acc[op][i][j], 0, 0, 0);
+        for (int op = 0; op < NB; ++op) {
+          if constexpr (I8)
+            acc[op][i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, f.b[op][i]),
+                                                                  __builtin_bit_cast(i32x4_t, f.a[j]), acc[op][i][j], 0, 0, 0);
+          else
+            acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[op][i], f.a[j], acc[op][i][j], 0, 0, 0);
+        }
   };
   // a workgroup barrier that no LDS access moves across (the waits are explicit)
   auto barrier = [] {
@@ -509,7 +521,7 @@ void ffn_product(FfnLaunch l) {
       if (*flag == 0u) return;                         // uniform
       __syncthreads();
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b) acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] = f32x4_t{};
+      for (int b = 0; b < BLOCKS; ++b) acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] = Acc{};
       for (int q = 0; q < splits; ++q) {
         const u64* from = tile_part + (int64_t)q * (BLOCKS * T::NT * 2) + tid * 2;
         u64 w[BLOCKS][2];
@@ -520,7 +532,7 @@ void ffn_product(FfnLaunch l) {
         }
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
-          f32x4_t o;
+          Acc o;
           __builtin_memcpy(&o, w[b], 16);
           acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] += o;
         }
@@ -540,6 +552,93 @@ void ffn_product(FfnLaunch l) {
   const int p2_row = lane / LPR, p2_col = 4 * (lane % LPR);
   const bool col_ok = wn0 + p2_col < ncols;
   const uint32_t col2 = (uint32_t)(wn0 + p2_col) * 2u;
+  if constexpr (I8) {
+    // Row scale before the block goes to LDS, column scale, bias, activation and residual in row order
+    // after it.  The sums are exact; their conversion to fp32 is the first rounding.
+    const I8Epilogue& q = l.ep;
+    float sx[T::FM];
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) {
+      const int ml = wm0 + 16 * j + (int)l16;
+      sx[j] = ml < mrows ? q.x_scale[m0 + ml] : 0.0f;
+    }
+    const int n = n0 + wn0 + p2_col;
+    f32x4_t sw = f32x4_t{}, bias = f32x4_t{};
+    if (col_ok) {                                      // (N is a multiple of 8: all four columns or none)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sw[e] = q.w_scale[n + e];
+        if (q.bias) bias[e] = q.wide ? ((const float*)q.bias)[n + e] : bf16_lo(((const uint16_t*)q.bias)[n + e]);
+      }
+    }
+    auto write = [&](auto act_c, auto wide_c) {
+      constexpr int A = decltype(act_c)::value;
+      constexpr bool WIDE = decltype(wide_c)::value;
+      constexpr uint32_t size = WIDE ? 4u : 2u;
+      auto rs_of = [&](const void* base, int64_t ld) {
+        return make_rsrc((const unsigned char*)base + ((int64_t)m0 * ld + n0) * size,
+                         ((int64_t)(uint32_t)(mrows - 1) * ld + ncols) * size);
+      };
+      const __amdgpu_buffer_rsrc_t y_rs = rs_of(p.Y, p.ldy), r_rs = p.E1 ? rs_of(p.E1, p.lde) : y_rs;
+      auto at = [&](int ml, int64_t ld) {
+        return (ml < mrows && col_ok) ? (uint32_t)ml * ((uint32_t)ld * size) + (uint32_t)(wn0 + p2_col) * size : kOOB;
+      };
+#pragma unroll
+      for (int j = 0; j < T::FM / 2; ++j) {
+        u32x4_t rv[PASSES];
+        if (p.E1) {
+#pragma unroll
+          for (int ps = 0; ps < PASSES; ++ps) {
+            const uint32_t off = at(wm0 + 32 * j + ps * RPP + p2_row, p.lde);
+            if constexpr (WIDE) {
+              rv[ps] = __builtin_amdgcn_raw_buffer_load_b128(r_rs, off, 0, 0);
+            } else {
+              const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(r_rs, off, 0, 0);
+              rv[ps] = u32x4_t{w[0] << 16, w[0] & 0xFFFF0000u, w[1] << 16, w[1] & 0xFFFF0000u};
+            }
+          }
+        }
+#pragma unroll
+        for (int par = 0; par < 2; ++par)
+#pragma unroll
+          for (int i = 0; i < T::FN; ++i) {
+            f32x4_t t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = (float)acc[0][i][2 * j + par][e] * sx[2 * j + par];
+            *(f32x4_t*)(ep + (16 * par + (int)l16) * T::EP_LD + 16 * i + 4 * (int)q16) = t;
+          }
+#pragma unroll
+        for (int ps = 0; ps < PASSES; ++ps) {
+          f32x4_t y = *(const f32x4_t*)(ep + (ps * RPP + p2_row) * T::EP_LD + p2_col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = gate<A>(fmaf(y[e], sw[e], bias[e]));
+            if (p.E1) y[e] += __uint_as_float(rv[ps][e]);
+          }
+          const uint32_t off = at(wm0 + 32 * j + ps * RPP + p2_row, p.ldy);
+          if constexpr (WIDE) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), y_rs, off, 0, 0);
+          } else {
+            u32x2_t w;
+            w[0] = pack_bf16x2(y[0], y[1]);
+            w[1] = pack_bf16x2(y[2], y[3]);
+            __builtin_amdgcn_raw_buffer_store_b64(w, y_rs, off, 0, 0);
+          }
+        }
+      }
+    };
+    auto by_type = [&](auto act_c) {
+      if (q.wide) write(act_c, std::true_type{});
+      else write(act_c, std::false_type{});
+    };
+    switch (q.act) {                                   // uniform
+      case ACT_RELU: by_type(std::integral_constant<int, ACT_RELU>{}); break;
+      case ACT_GELU_TANH: by_type(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+      case ACT_SILU: by_type(std::integral_constant<int, ACT_SILU>{}); break;
+      default: by_type(std::integral_constant<int, ACT_NONE>{}); break;
+    }
+    return;
+  } else {
   auto out_rs = [&](uint16_t* base, int64_t ld) {
     return make_rsrc(base + (int64_t)m0 * ld + n0, (int64_t)(uint32_t)(mrows - 1) * ld * 2 + ncols * 2);
   };
@@ -646,6 +745,7 @@ void ffn_product(FfnLaunch l) {
         store(y, y_rs, offset(wm0 + 32 * j + ps * RPP + p2_row, p.ldy));
       }
     }
+  }
   }
 }
 

@@ -1,0 +1,113 @@
+// Layer norm of rows, with dropout and residual add in front of it: the forward pass (gfx950).
+//
+// Memory-bound: X and R are read once, S and Y written once.  A row lies in the registers of 64 to 1024
+// threads (RowShape) from its loads to its stores; its mean and the mean square of what is left are two
+// sums over those threads, one after the other, so that rows far from zero lose nothing.
+#include "ge_rows_common.h"
+
+namespace ge {
+namespace {
+
+template <class E, int TR, int V, bool TAIL, bool DROP>
+__global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p) {
+  constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
+  __shared__ float red[2][NT / 64];
+  const int t = (int)threadIdx.x % TR, sub = (int)threadIdx.x / TR, d = p.d;
+  const uint32_t blocks = (uint32_t)(d + 7) / 8u;
+  const float of_d = (float)d;
+  DropKey key{};
+  if constexpr (DROP) key = drop_key(p.drop);
+  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < p.rows; row += (int64_t)gridDim.x * RPW) {
+    const E* x = (const E*)p.x + row * p.ldx;
+    float v[V][8];
+    Raw<E> raw[V], rr[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) raw[i] = fetch<E, TAIL>(x, 8 * (t + TR * i), d);
+    if (p.r) {                                         // uniform
+#pragma unroll
+      for (int i = 0; i < V; ++i) rr[i] = fetch<E, TAIL>((const E*)p.r + row * p.ldr, 8 * (t + TR * i), d);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      Words w{};
+      if constexpr (DROP) w = philox((uint32_t)row * blocks + (uint32_t)(t + TR * i), p.drop.site, key);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = get(raw[i], j);
+        if constexpr (DROP) v[i][j] = dropped(v[i][j], w, j, p.drop);
+        if (p.r) v[i][j] += get(rr[i], j);
+      }
+      // the norm is that of the sum as it is kept
+      const Raw<E> kept = rounded(v[i], E());
+      if (p.s) put<E, TAIL>((E*)p.s + row * p.lds, 8 * (t + TR * i), d, kept);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = get(kept, j);
+        sum += v[i][j];
+      }
+    }
+    const float mean = row_sum<TR>(sum, red[0]) / of_d;
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = 8 * (t + TR * i) + j < d ? v[i][j] - mean : 0.0f;
+        sq = fmaf(v[i][j], v[i][j], sq);
+      }
+    const float var = row_sum<TR>(sq, red[1]) / of_d, rstd = 1.0f / sqrtf(var + p.eps);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int col = 8 * (t + TR * i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
+      if (p.gain) {
+        const Raw<E> g = fetch<E, TAIL>((const E*)p.gain, col, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= get(g, j);
+      }
+      if (p.bias) {
+        const Raw<E> b = fetch<E, TAIL>((const E*)p.bias, col, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += get(b, j);
+      }
+      put<E, TAIL>((E*)p.y + row * p.ldy, col, d, rounded(v[i], E()));
+    }
+  }
+}
+
+template <class E, int S, bool TAIL>
+hipError_t go(const NormParams& p, int grid, hipStream_t s) {
+  constexpr int TR = kRowShape[S].threads, V = kRowShape[S].vecs;
+  const dim3 g((unsigned)grid), b(TR < 256 ? 256 : TR);
+  if (p.drop.below) hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, false>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+template <class E, bool TAIL>
+hipError_t by_shape(const NormParams& p, int grid, hipStream_t s) {
+  switch (row_shape(p.d)) {
+    case 0: return go<E, 0, TAIL>(p, grid, s);
+    case 1: return go<E, 1, TAIL>(p, grid, s);
+    case 2: return go<E, 2, TAIL>(p, grid, s);
+    case 3: return go<E, 3, TAIL>(p, grid, s);
+    case 4: return go<E, 4, TAIL>(p, grid, s);
+    case 5: return go<E, 5, TAIL>(p, grid, s);
+    default: return go<E, 6, TAIL>(p, grid, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(bool bf16, const NormParams& p, int grid, hipStream_t s) {
+  if (grid <= 0) return hipSuccess;
+  if (bf16) return p.d % 8 ? by_shape<uint16_t, true>(p, grid, s) : by_shape<uint16_t, false>(p, grid, s);
+  return p.d % 8 ? by_shape<float, true>(p, grid, s) : by_shape<float, false>(p, grid, s);
+}
+
+}  // namespace ge

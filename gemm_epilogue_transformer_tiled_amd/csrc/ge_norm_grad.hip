@@ -1,0 +1,184 @@
+// Layer norm of rows: the backward pass with the sums of the gain's and the bias' gradients (gfx950).
+//
+// Memory-bound: dY, S (and dS) are read once, dX (and dR) written once.  A row lies in registers as in the
+// forward pass; mean(e) and mean(e n) are taken in one exchange.  A thread holds the same columns of every
+// row, so it adds up dgain and dbias of its columns in registers over all rows of its workgroup, and
+// a workgroup leaves one partial sum per column; a second launch adds these in 64 bits, in a fixed order.
+#include "ge_rows_common.h"
+
+namespace ge {
+namespace {
+
+template <class E, int TR, int V, bool TAIL, bool DROP>
+__global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradParams p) {
+  constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
+  __shared__ float red[2][2][NT / 64];
+  __shared__ float gsum[RPW > 1 ? (RPW - 1) * 8 * TR * V : 1];
+  const int t = (int)threadIdx.x % TR, sub = (int)threadIdx.x / TR, d = p.d;
+  const uint32_t blocks = (uint32_t)(d + 7) / 8u;
+  const float of_d = (float)d;
+  DropKey key{};
+  if constexpr (DROP) key = drop_key(p.drop);
+  float dgain[V][8], dbias[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dgain[i][j] = dbias[i][j] = 0.0f;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < p.rows; row += (int64_t)gridDim.x * RPW, turn ^= 1) {
+    Raw<E> rdy[V], rs[V], rds[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int col = 8 * (t + TR * i);
+      rdy[i] = fetch<E, TAIL>((const E*)p.dy + row * p.lddy, col, d);
+      rs[i] = fetch<E, TAIL>((const E*)p.s + row * p.lds, col, d);
+      if (p.ds) rds[i] = fetch<E, TAIL>((const E*)p.ds + row * p.ldds, col, d);
+    }
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float e[V][8], n[V][8], se = 0.0f, sen = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      Raw<E> g;
+      if (p.gain) g = fetch<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // (past the row's end dy is 0: whatever n is there, it adds nothing)
+        const float dy = get(rdy[i], j);
+        n[i][j] = (get(rs[i], j) - mean) * rstd;
+        e[i][j] = p.gain ? dy * get(g, j) : dy;
+        se += e[i][j];
+        sen = fmaf(e[i][j], n[i][j], sen);
+        dgain[i][j] = fmaf(dy, n[i][j], dgain[i][j]);
+        dbias[i][j] += dy;
+      }
+    }
+    se = wave_sum(se);
+    sen = wave_sum(sen);
+    if constexpr (TR > 64) {
+      const int w = (int)threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        red[turn][0][w] = se;
+        red[turn][1][w] = sen;
+      }
+      __syncthreads();
+      se = sen = 0.0f;
+#pragma unroll
+      for (int k = 0; k < TR / 64; ++k) {
+        se += red[turn][0][k];
+        sen += red[turn][1][k];
+      }
+    }
+    const float me = se / of_d, men = sen / of_d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int col = 8 * (t + TR * i);
+      float g[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] = rstd * fmaf(-n[i][j], men, e[i][j] - me);
+        if (p.ds) g[j] += get(rds[i], j);
+      }
+      if (p.dr) put<E, TAIL>((E*)p.dr + row * p.lddr, col, d, rounded(g, E()));
+      if (p.dx) {
+        if constexpr (DROP) {
+          const Words w = philox((uint32_t)row * blocks + (uint32_t)(t + TR * i), p.drop.site, key);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = dropped(g[j], w, j, p.drop);
+        }
+        put<E, TAIL>((E*)p.dx + row * p.lddx, col, d, rounded(g, E()));
+      }
+    }
+  }
+  if (!p.part) return;                                 // uniform
+  float* const out = p.part + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float(&a)[V][8] = which ? dbias : dgain;
+    if constexpr (RPW > 1) {
+      // the rows taken at once meet in LDS and are added in their order
+      if (which) __syncthreads();
+      if (sub > 0)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gsum[((sub - 1) * V * 8 + i * 8 + j) * TR + t] = a[i][j];
+      __syncthreads();
+      if (sub == 0)
+        for (int q = 0; q < RPW - 1; ++q)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[i][j] += gsum[(q * V * 8 + i * 8 + j) * TR + t];
+    }
+    if (sub == 0)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int col = 8 * (t + TR * i) + j;
+          if (col < d) out[which * d + col] = a[i][j];
+        }
+  }
+}
+
+// Adds the workgroups' partial sums, 32 columns a workgroup, 32 threads a column.
+__global__ __launch_bounds__(1024) void norm_sums(const float* part, int parts, int d, float* dgain, float* dbias) {
+  __shared__ double sums[32][33];
+  const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + c, cols = 2 * d;
+  double s = 0.0;
+  if (col < cols) {
+    int r = r0;
+    for (; r + 96 < parts; r += 128) {                 // four loads on their way
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(int64_t)(r + 32 * u) * cols + col];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s += (double)v[u];
+    }
+    for (; r < parts; r += 32) s += (double)part[(int64_t)r * cols + col];
+  }
+  sums[r0][c] = s;
+  __syncthreads();
+  if (r0 == 0 && col < cols) {
+    double all = 0.0;
+    for (int r = 0; r < 32; ++r) all += sums[r][c];
+    float* out = col < d ? dgain : dbias;
+    if (out) out[col < d ? col : col - d] = (float)all;
+  }
+}
+
+template <class E, int S, bool TAIL>
+hipError_t go(const NormGradParams& p, int grid, hipStream_t s) {
+  constexpr int TR = kRowShape[S].threads, V = kRowShape[S].vecs;
+  const dim3 g((unsigned)grid), b(TR < 256 ? 256 : TR);
+  if (p.drop.below) hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, false>), g, b, 0, s, p);
+  return hipGetLastError();
+}
+template <class E, bool TAIL>
+hipError_t by_shape(const NormGradParams& p, int grid, hipStream_t s) {
+  switch (row_shape(p.d)) {
+    case 0: return go<E, 0, TAIL>(p, grid, s);
+    case 1: return go<E, 1, TAIL>(p, grid, s);
+    case 2: return go<E, 2, TAIL>(p, grid, s);
+    case 3: return go<E, 3, TAIL>(p, grid, s);
+    case 4: return go<E, 4, TAIL>(p, grid, s);
+    case 5: return go<E, 5, TAIL>(p, grid, s);
+    default: return go<E, 6, TAIL>(p, grid, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm_backward(bool bf16, const NormGradParams& p, int grid, hipStream_t s) {
+  if (grid <= 0) return hipSuccess;
+  if (bf16) return p.d % 8 ? by_shape<uint16_t, true>(p, grid, s) : by_shape<uint16_t, false>(p, grid, s);
+  return p.d % 8 ? by_shape<float, true>(p, grid, s) : by_shape<float, false>(p, grid, s);
+}
+
+hipError_t launch_norm_sums(const float* part, int parts, int d, float* dgain, float* dbias, hipStream_t s) {
+  hipLaunchKernelGGL(norm_sums, dim3((unsigned)((2 * d + 31) / 32)), dim3(1024), 0, s, part, parts, d, dgain, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace ge

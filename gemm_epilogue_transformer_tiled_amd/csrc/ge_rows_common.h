@@ -1,0 +1,159 @@
+// Device helpers of the row operators: vectors of eight values, sums over the threads of a row, and
+// dropout's random numbers.
+#pragma once
+
+#include "ge_rows_internal.h"
+
+namespace ge {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+// wide accesses at the elements' alignment: rows start anywhere
+typedef u32x4 Any16 __attribute__((aligned(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const bf16x2 h = {(__bf16)a, (__bf16)b};      // round to nearest even
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// Eight values as they lie in memory.
+template <class E>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 w;
+};
+template <>
+struct Raw<float> {
+  u32x4 w, w2;
+};
+
+template <class E>
+__device__ __forceinline__ Raw<E> zero() {
+  Raw<E> r;
+  r.w = u32x4{0, 0, 0, 0};
+  if constexpr (sizeof(E) == 4) r.w2 = u32x4{0, 0, 0, 0};
+  return r;
+}
+
+__device__ __forceinline__ float get(const Raw<uint16_t>& r, int j) { return (j & 1) ? hi(r.w[j >> 1]) : lo(r.w[j >> 1]); }
+__device__ __forceinline__ float get(const Raw<float>& r, int j) { return __uint_as_float(j < 4 ? r.w[j] : r.w2[j - 4]); }
+__device__ __forceinline__ Raw<uint16_t> rounded(const float (&v)[8], uint16_t) {
+  Raw<uint16_t> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.w[j] = pack2(v[2 * j], v[2 * j + 1]);
+  return r;
+}
+__device__ __forceinline__ Raw<float> rounded(const float (&v)[8], float) {
+  Raw<float> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r.w[j] = __float_as_uint(v[j]);
+    r.w2[j] = __float_as_uint(v[4 + j]);
+  }
+  return r;
+}
+
+// Values col .. col + 7 of a row of d; zeros past its end.  TAIL: d is no multiple of eight, so the row's last
+// vector is read and written value by value.
+template <class E, bool TAIL>
+__device__ __forceinline__ Raw<E> fetch(const E* row, int col, int d) {
+  Raw<E> r = zero<E>();
+  if (col + (TAIL ? 8 : 1) <= d) {
+    r.w = *(const Any16*)(row + col);
+    if constexpr (sizeof(E) == 4) r.w2 = *(const Any16*)(row + col + 4);
+  } else if (TAIL && col < d) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < d) {
+        if constexpr (sizeof(E) == 2) r.w[j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
+        else if (j < 4) r.w[j] = __float_as_uint(row[col + j]);
+        else r.w2[j - 4] = __float_as_uint(row[col + j]);
+      }
+  }
+  return r;
+}
+template <class E, bool TAIL>
+__device__ __forceinline__ void put(E* row, int col, int d, const Raw<E>& r) {
+  if (col + (TAIL ? 8 : 1) <= d) {
+    *(Any16*)(row + col) = r.w;
+    if constexpr (sizeof(E) == 4) *(Any16*)(row + col + 4) = r.w2;
+  } else if (TAIL && col < d) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < d) {
+        if constexpr (sizeof(E) == 2) row[col + j] = (uint16_t)(r.w[j >> 1] >> (16 * (j & 1)));
+        else row[col + j] = get(r, j);
+      }
+  }
+}
+
+// Sum over a wave, the same bits in every lane: exchanges within 16 lanes are DPP operands of the adds
+// (after the first two steps quads agree, so mirrored halves stand for the further ones).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1>(v);       // quad: lanes 1 0 3 2
+  v = dpp_add<0x4E>(v);       // quad: lanes 2 3 0 1
+  v = dpp_add<0x141>(v);      // mirrored in 8
+  v = dpp_add<0x140>(v);      // mirrored in 16
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// Sum over the TR threads of a row.  `lds`: one word a wave; a place that alternates from call to call, so
+// that one barrier is enough (a wave writes a place again only after the barrier of the other, which
+// every wave reaches with its reads of the first done).
+template <int TR>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+  v = wave_sum(v);
+  if constexpr (TR == 64) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = lds[0];
+#pragma unroll
+  for (int w = 1; w < TR / 64; ++w) v += lds[w];
+  return v;
+}
+
+// ---- dropout ----
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011): ten rounds of two 32 x 32 -> 64-bit products.  The
+// products' rate is a quarter of the adds', so a value gets 16 bits, not 32: one call serves eight.
+struct Words {
+  uint32_t w[4];
+};
+struct DropKey {
+  uint32_t k0, k1, o0, o1;    // seed, offset (uniform)
+};
+__device__ __forceinline__ DropKey drop_key(const DropParams& p) {
+  const uint32_t* q = (const uint32_t*)p.rng;
+  return DropKey{(uint32_t)__builtin_amdgcn_readfirstlane((int)q[0]), (uint32_t)__builtin_amdgcn_readfirstlane((int)q[1]),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)q[2]), (uint32_t)__builtin_amdgcn_readfirstlane((int)q[3])};
+}
+__device__ __forceinline__ Words philox(uint32_t block, uint32_t site, const DropKey& key) {
+  uint32_t c0 = block, c1 = site, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return Words{{c0, c1, c2, c3}};
+}
+// Value j of the block: 0 where dropped (a NaN too), times the factor elsewhere.
+__device__ __forceinline__ float dropped(float v, const Words& w, int j, const DropParams& p) {
+  const uint32_t h = (j & 1) ? w.w[j >> 1] >> 16 : w.w[j >> 1] & 0xFFFFu;
+  return h < p.below ? 0.0f : v * p.factor;
+}
+
+}  // namespace
+}  // namespace ge

@@ -1,0 +1,76 @@
+// Internal interface between the C-ABI of the row operators (rows_api.cpp) and their HIP kernels.
+#pragma once
+
+#include "ge_block_internal.h"
+
+namespace ge {
+
+// ---- how a row lies on threads ----
+// Eight values are a vector; thread t of a row's `threads` holds vectors t, t + threads, ... up to `vecs`
+// of them.  So a wave reads 1 KB of bf16 at a time, and the whole row is in registers between its
+// sums and its outputs.
+struct RowShape { int threads, vecs; };
+constexpr int kRowShapes = 7;
+constexpr RowShape kRowShape[kRowShapes] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2}, {1024, 2}, {1024, 4}};
+constexpr int64_t kRowMax = 8 * 1024 * 4;
+inline int row_shape(int64_t d) {
+  for (int i = 0; i < kRowShapes - 1; ++i)
+    if (d <= 8 * kRowShape[i].threads * kRowShape[i].vecs) return i;
+  return kRowShapes - 1;
+}
+// Rows a workgroup takes at a time: workgroups have 256 threads at least.
+inline int rows_at_once(int shape) { return kRowShape[shape].threads < 256 ? 256 / kRowShape[shape].threads : 1; }
+
+struct DropParams {
+  const int64_t* rng;         // seed, offset
+  uint32_t site, below;       // dropped: half-words below `below` (0: no dropout)
+  float factor;               // of kept values
+};
+
+struct NormParams {
+  const void *x, *r;          // r NULL: no residual
+  void *s, *y;                // s NULL: not kept
+  const void *gain, *bias;    // NULL: ones, zeros
+  float *mean, *rstd;         // NULL: not kept
+  DropParams drop;
+  int64_t rows, ldx, ldr, lds, ldy;
+  int32_t d;
+  float eps;
+};
+struct NormGradParams {
+  const void *dy, *s, *ds;    // ds NULL: none
+  const void* gain;           // NULL: ones
+  const float *mean, *rstd;
+  void *dx, *dr;              // NULL: not computed
+  float* part;                // [workgroups][2][d]: dgain, dbias; NULL: not computed
+  DropParams drop;
+  int64_t rows, lddy, lds, ldds, lddx, lddr;
+  int32_t d;
+};
+hipError_t launch_norm_forward(bool bf16, const NormParams& p, int grid, hipStream_t s);
+hipError_t launch_norm_backward(bool bf16, const NormGradParams& p, int grid, hipStream_t s);
+// parts partial sums of both -> dgain, dbias (either may be NULL)
+hipError_t launch_norm_sums(const float* part, int parts, int d, float* dgain, float* dbias, hipStream_t s);
+
+struct DropoutParams {
+  const void *x, *r;
+  void* y;
+  DropParams drop;
+  int64_t rows, ldx, ldr, ldy;
+  int32_t d;
+};
+hipError_t launch_dropout(bool bf16, const DropoutParams& p, hipStream_t s);
+
+struct QuantParams {
+  const void* x;
+  int8_t* codes;
+  float* scale;
+  int64_t rows, ldx, ldq;
+  int32_t d;
+};
+hipError_t launch_quant(bool bf16, const QuantParams& p, int grid, hipStream_t s);
+
+// ---- product of codes: tiles of ge_ffn_impl.h (FfnTile), sizes and pitches of X and W in 2-byte units ----
+hipError_t launch_i8(int tile, const I8Launch& l, hipStream_t s);
+
+}  // namespace ge
