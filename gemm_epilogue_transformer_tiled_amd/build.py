@@ -23,7 +23,7 @@ TWO_WAVE = [f"ge_tile_{t}_{lay}.hip" for t in ("256x256w8", "256x128w8_pair") fo
 COMMON = ["ge_kernels.hip", "noalloc.hip", "tiles.cpp", "api.cpp"]
 BLOCK = ["ge_ffn_pair.hip", "ge_ffn_grad.hip", "ge_ffn_plain.hip", "ge_ffn_few.hip", "ge_qk.hip", "ge_clip.hip", "block_api.cpp",
          "block_rowwise_api.cpp"]
-ROWS = ["ge_norm.hip", "ge_norm_grad.hip", "ge_dropout.hip", "ge_quant.hip", "ge_i8.hip", "rows_api.cpp"]
+ROWS = ["ge_norm.hip", "ge_norm_grad.hip", "ge_dropout.hip", "ge_quant.hip", "ge_i8.hip", "ge_i8_few.hip", "rows_api.cpp"]
 # library -> (its sources, extra compiler flags)
 TARGETS = {
     os.path.join(HERE, "libgemm_epilogue.so"): (ONE_WAVE + TWO_WAVE + COMMON, ()),

@@ -9,9 +9,10 @@ namespace ge {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
 
 // FLAT: dense rows of whole vectors: block i is elements 8 i .. 8 i + 7.
-template <class E, bool FLAT, bool TAIL, bool RES>
+template <class E, bool FLAT, bool TAIL, bool RES, int POLICY>
 __global__ __launch_bounds__(kThreads) void dropout(DropoutParams p) {
   const DropKey key = drop_key(p.drop);
   const uint32_t blocks = (uint32_t)(p.d + 7) / 8u;
@@ -22,9 +23,9 @@ __global__ __launch_bounds__(kThreads) void dropout(DropoutParams p) {
     const E* x = (const E*)p.x + (FLAT ? 8 * i : (int64_t)row * p.ldx);
     const E* r = (const E*)p.r + (FLAT ? 8 * i : (int64_t)row * p.ldr);
     E* y = (E*)p.y + (FLAT ? 8 * i : (int64_t)row * p.ldy);
-    const Raw<E> rx = fetch<E, TAIL>(x, col, d);
+    const Raw<E> rx = fetch<E, TAIL, POLICY>(x, col, d);
     Raw<E> rr;
-    if constexpr (RES) rr = fetch<E, TAIL>(r, col, d);
+    if constexpr (RES) rr = fetch<E, TAIL, POLICY>(r, col, d);
     const Words w = philox(b, p.drop.site, key);
     float v[8];
 #pragma unroll
@@ -32,27 +33,28 @@ __global__ __launch_bounds__(kThreads) void dropout(DropoutParams p) {
       v[j] = dropped(get(rx, j), w, j, p.drop);
       if constexpr (RES) v[j] += get(rr, j);
     }
-    put<E, TAIL>(y, col, d, rounded(v, E()));
+    put<E, TAIL, POLICY>(y, col, d, rounded(v, E()));
   }
 }
 
 template <class E, bool RES>
-hipError_t go(const DropoutParams& p, hipStream_t s) {
+hipError_t go(bool large, const DropoutParams& p, hipStream_t s) {
   const int64_t n = p.rows * ((p.d + 7) / 8), groups = (n + kThreads - 1) / kThreads;
-  const dim3 g((unsigned)(groups < 4096 ? groups : 4096)), b(kThreads);
+  const dim3 g((unsigned)(groups < 16384 ? groups : 16384)), b(kThreads);
   const bool flat = p.d % 8 == 0 && p.ldx == p.d && p.ldy == p.d && (!RES || p.ldr == p.d);
-  if (flat) hipLaunchKernelGGL((dropout<E, true, false, RES>), g, b, 0, s, p);
-  else if (p.d % 8) hipLaunchKernelGGL((dropout<E, false, true, RES>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((dropout<E, false, false, RES>), g, b, 0, s, p);
+  if (flat && large) hipLaunchKernelGGL((dropout<E, true, false, RES, kLarge>), g, b, 0, s, p);
+  else if (flat) hipLaunchKernelGGL((dropout<E, true, false, RES, 0>), g, b, 0, s, p);
+  else if (p.d % 8) hipLaunchKernelGGL((dropout<E, false, true, RES, 0>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((dropout<E, false, false, RES, 0>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_dropout(bool bf16, const DropoutParams& p, hipStream_t s) {
+hipError_t launch_dropout(bool bf16, bool large, const DropoutParams& p, hipStream_t s) {
   if (p.rows <= 0 || p.d <= 0) return hipSuccess;
-  if (bf16) return p.r ? go<uint16_t, true>(p, s) : go<uint16_t, false>(p, s);
-  return p.r ? go<float, true>(p, s) : go<float, false>(p, s);
+  if (bf16) return p.r ? go<uint16_t, true>(large, p, s) : go<uint16_t, false>(large, p, s);
+  return p.r ? go<float, true>(large, p, s) : go<float, false>(large, p, s);
 }
 
 }  // namespace ge

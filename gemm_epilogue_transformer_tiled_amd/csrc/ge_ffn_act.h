@@ -14,4 +14,13 @@ __device__ __forceinline__ float gate(float z) {
   else return activate<ACT>(z);
 }
 
+// An output of the product of codes from its sum times the row's scale.  One function for all its kernels, and
+// the residual never fused into the activation's last product: every tile gives the same bits.
+template <int ACT>
+__device__ __forceinline__ float i8_output(float sum, float w_scale, float bias, float residual) {
+#pragma clang fp contract(off)
+  const float y = gate<ACT>(__builtin_fmaf(sum, w_scale, bias));
+  return y + residual;
+}
+
 }  // namespace ge

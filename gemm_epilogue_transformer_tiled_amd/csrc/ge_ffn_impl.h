@@ -355,6 +355,26 @@ void ffn_product(LAUNCH l) {
             acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[op][i], f.a[j], acc[op][i][j], 0, 0, 0);
         }
   };
+  // The scales and the bias of the product of codes: loaded here, a trip to memory before they are needed.
+  // (four columns of the epilogue's second phase a lane; N is a multiple of 8: all four or none)
+  float i8_sx[I8 ? T::FM : 1];
+  f32x4_t i8_sw = f32x4_t{}, i8_bias = f32x4_t{};
+  if constexpr (I8) {
+    const I8Epilogue& q = l.ep;
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) {
+      const int ml = wm0 + 16 * j + (int)l16;
+      i8_sx[j] = ml < mrows ? q.x_scale[m0 + ml] : 0.0f;
+    }
+    const int col = wn0 + 4 * (lane % (T::WN / 4)), n = n0 + col;
+    if (col < ncols) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        i8_sw[e] = q.w_scale[n + e];
+        if (q.bias) i8_bias[e] = q.wide ? ((const float*)q.bias)[n + e] : bf16_lo(((const uint16_t*)q.bias)[n + e]);
+      }
+    }
+  }
   // a workgroup barrier that no LDS access moves across (the waits are explicit)
   auto barrier = [] {
     asm volatile("" ::: "memory");
@@ -422,9 +442,12 @@ void ffn_product(LAUNCH l) {
       mem_phase(s_c, j);
       mat_phase();
     };
-    // whole rings: four steps (A and a column B), twelve with a row B's three arrays
+    // Whole rings: four steps (A and a column B), twelve with a row B's three arrays; steps past the end
+    // multiply zeros.  Codes have half as many steps for the same contraction, so there the last ring ends
+    // with the last slot.
     constexpr int RING = BC ? 4 : 12;
-    for (int j = 0; j < nk; j += RING) {
+    int j = 0;
+    for (; I8 ? j + RING <= nk : j < nk; j += RING) {
       step(GE_I(0), j);
       step(GE_I(1), j + 1);
       step(GE_I(2), j + 2);
@@ -438,6 +461,28 @@ void ffn_product(LAUNCH l) {
         step(GE_I(9), j + 9);
         step(GE_I(10), j + 10);
         step(GE_I(11), j + 11);
+      }
+    }
+    if constexpr (I8) {
+      if (j < nk) {
+        step(GE_I(0), j);
+        step(GE_I(1), j + 1);
+        if (j + 2 < nk) {
+          step(GE_I(2), j + 2);
+          step(GE_I(3), j + 3);
+          if (j + 4 < nk) {
+            step(GE_I(4), j + 4);
+            step(GE_I(5), j + 5);
+            if (j + 6 < nk) {
+              step(GE_I(6), j + 6);
+              step(GE_I(7), j + 7);
+              if (j + 8 < nk) {
+                step(GE_I(8), j + 8);
+                step(GE_I(9), j + 9);
+              }
+            }
+          }
+        }
       }
     }
     if (grp == 0) barrier();
@@ -500,13 +545,19 @@ void ffn_product(LAUNCH l) {
       typedef unsigned long long u64;
       constexpr int BLOCKS = NB * T::FN * T::FM;
       u64* const tile_part = (u64*)l.part + (int64_t)tile_id * splits * (BLOCKS * T::NT * 2);
-      u64* const mine = tile_part + (int64_t)split * (BLOCKS * T::NT * 2) + tid * 2;
+      // int32 sums: a store's lanes write one run of memory, and blocks of rows past the last one are left out
+      constexpr int LANE = I8 ? 1 : 2, HALF = I8 ? T::NT : 1;
+      auto kept = [&](int b) { return !I8 || wm0 + 16 * (b % T::FM) < mrows; };
+      u64* const mine = tile_part + (int64_t)split * (BLOCKS * T::NT * 2) + tid * LANE;
 #pragma unroll
       for (int b = 0; b < BLOCKS; ++b) {
+        if constexpr (I8) {
+          if (!kept(b)) continue;                      // uniform
+        }
         u64 w[2];
         __builtin_memcpy(w, &acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM], 16);
         __hip_atomic_store(mine + b * (T::NT * 2), w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(mine + b * (T::NT * 2) + 1, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(mine + b * (T::NT * 2) + HALF, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       __builtin_amdgcn_s_waitcnt(kVmcnt0);
       __syncthreads();
@@ -520,6 +571,34 @@ void ffn_product(LAUNCH l) {
       __syncthreads();
       if (*flag == 0u) return;                         // uniform
       __syncthreads();
+      if constexpr (I8) {
+        // This workgroup's sums are at hand; the others' are loaded AHEAD splits at a time.
+        constexpr int AHEAD = BLOCKS > 4 ? 2 : 4;
+        for (int q0 = 0; q0 < splits; q0 += AHEAD) {
+          u64 w[AHEAD][BLOCKS][2];
+#pragma unroll
+          for (int q = 0; q < AHEAD; ++q) {
+            const u64* from = tile_part + (int64_t)(q0 + q) * (BLOCKS * T::NT * 2) + tid;
+            const bool other = q0 + q < splits && q0 + q != split;           // uniform
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+              w[q][b][0] = w[q][b][1] = 0;
+              if (other && kept(b)) {
+                w[q][b][0] = __hip_atomic_load(from + b * (T::NT * 2), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                w[q][b][1] = __hip_atomic_load(from + b * (T::NT * 2) + T::NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+              Acc o;
+              __builtin_memcpy(&o, w[q][b], 16);
+              acc[0][b / T::FM][b % T::FM] += o;
+            }
+        }
+      } else {
 #pragma unroll
       for (int b = 0; b < BLOCKS; ++b) acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] = Acc{};
       for (int q = 0; q < splits; ++q) {
@@ -536,6 +615,7 @@ void ffn_product(LAUNCH l) {
           __builtin_memcpy(&o, w[b], 16);
           acc[b / (T::FN * T::FM)][b / T::FM % T::FN][b % T::FM] += o;
         }
+      }
       }
     }
   }
@@ -556,25 +636,12 @@ void ffn_product(LAUNCH l) {
     // Row scale before the block goes to LDS, column scale, bias, activation and residual in row order
     // after it.  The sums are exact; their conversion to fp32 is the first rounding.
     const I8Epilogue& q = l.ep;
-    float sx[T::FM];
-#pragma unroll
-    for (int j = 0; j < T::FM; ++j) {
-      const int ml = wm0 + 16 * j + (int)l16;
-      sx[j] = ml < mrows ? q.x_scale[m0 + ml] : 0.0f;
-    }
-    const int n = n0 + wn0 + p2_col;
-    f32x4_t sw = f32x4_t{}, bias = f32x4_t{};
-    if (col_ok) {                                      // (N is a multiple of 8: all four columns or none)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sw[e] = q.w_scale[n + e];
-        if (q.bias) bias[e] = q.wide ? ((const float*)q.bias)[n + e] : bf16_lo(((const uint16_t*)q.bias)[n + e]);
-      }
-    }
     auto write = [&](auto act_c, auto wide_c) {
       constexpr int A = decltype(act_c)::value;
       constexpr bool WIDE = decltype(wide_c)::value;
       constexpr uint32_t size = WIDE ? 4u : 2u;
+      // stores of the largest tiles go "nt": their outputs pass what the caches keep (8192 x 4096 x 11008: 323 -> 317 us)
+      constexpr int NT = T::PP ? 2 : 0;
       auto rs_of = [&](const void* base, int64_t ld) {
         return make_rsrc((const unsigned char*)base + ((int64_t)m0 * ld + n0) * size,
                          ((int64_t)(uint32_t)(mrows - 1) * ld + ncols) * size);
@@ -604,7 +671,7 @@ void ffn_product(LAUNCH l) {
           for (int i = 0; i < T::FN; ++i) {
             f32x4_t t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = (float)acc[0][i][2 * j + par][e] * sx[2 * j + par];
+            for (int e = 0; e < 4; ++e) t[e] = (float)acc[0][i][2 * j + par][e] * i8_sx[2 * j + par];
             *(f32x4_t*)(ep + (16 * par + (int)l16) * T::EP_LD + 16 * i + 4 * (int)q16) = t;
           }
 #pragma unroll
@@ -612,17 +679,16 @@ void ffn_product(LAUNCH l) {
           f32x4_t y = *(const f32x4_t*)(ep + (ps * RPP + p2_row) * T::EP_LD + p2_col);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            y[e] = gate<A>(fmaf(y[e], sw[e], bias[e]));
-            if (p.E1) y[e] += __uint_as_float(rv[ps][e]);
+            y[e] = i8_output<A>(y[e], i8_sw[e], i8_bias[e], p.E1 ? __uint_as_float(rv[ps][e]) : -0.0f);
           }
           const uint32_t off = at(wm0 + 32 * j + ps * RPP + p2_row, p.ldy);
           if constexpr (WIDE) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), y_rs, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), y_rs, off, 0, NT);
           } else {
             u32x2_t w;
             w[0] = pack_bf16x2(y[0], y[1]);
             w[1] = pack_bf16x2(y[2], y[3]);
-            __builtin_amdgcn_raw_buffer_store_b64(w, y_rs, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(w, y_rs, off, 0, NT);
           }
         }
       }

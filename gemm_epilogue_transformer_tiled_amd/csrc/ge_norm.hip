@@ -8,7 +8,9 @@
 namespace ge {
 namespace {
 
-template <class E, int TR, int V, bool TAIL, bool DROP>
+constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
+
+template <class E, int TR, int V, bool TAIL, bool DROP, int POLICY>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
   __shared__ float red[2][NT / 64];
@@ -22,10 +24,10 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p
     float v[V][8];
     Raw<E> raw[V], rr[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) raw[i] = fetch<E, TAIL>(x, 8 * (t + TR * i), d);
+    for (int i = 0; i < V; ++i) raw[i] = fetch<E, TAIL, POLICY>(x, 8 * (t + TR * i), d);
     if (p.r) {                                         // uniform
 #pragma unroll
-      for (int i = 0; i < V; ++i) rr[i] = fetch<E, TAIL>((const E*)p.r + row * p.ldr, 8 * (t + TR * i), d);
+      for (int i = 0; i < V; ++i) rr[i] = fetch<E, TAIL, POLICY>((const E*)p.r + row * p.ldr, 8 * (t + TR * i), d);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -40,7 +42,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p
       }
       // the norm is that of the sum as it is kept
       const Raw<E> kept = rounded(v[i], E());
-      if (p.s) put<E, TAIL>((E*)p.s + row * p.lds, 8 * (t + TR * i), d, kept);
+      if (p.s) put<E, TAIL, POLICY>((E*)p.s + row * p.lds, 8 * (t + TR * i), d, kept);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[i][j] = get(kept, j);
@@ -76,38 +78,42 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += get(b, j);
       }
-      put<E, TAIL>((E*)p.y + row * p.ldy, col, d, rounded(v[i], E()));
+      put<E, TAIL, POLICY>((E*)p.y + row * p.ldy, col, d, rounded(v[i], E()));
     }
   }
 }
 
-template <class E, int S, bool TAIL>
+template <class E, int S, bool TAIL, int POLICY>
 hipError_t go(const NormParams& p, int grid, hipStream_t s) {
   constexpr int TR = kRowShape[S].threads, V = kRowShape[S].vecs;
   const dim3 g((unsigned)grid), b(TR < 256 ? 256 : TR);
-  if (p.drop.below) hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, true>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, false>), g, b, 0, s, p);
+  if (p.drop.below) hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, true, POLICY>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((norm_forward<E, TR, V, TAIL, false, POLICY>), g, b, 0, s, p);
   return hipGetLastError();
 }
-template <class E, bool TAIL>
+template <class E, bool TAIL, int POLICY>
 hipError_t by_shape(const NormParams& p, int grid, hipStream_t s) {
   switch (row_shape(p.d)) {
-    case 0: return go<E, 0, TAIL>(p, grid, s);
-    case 1: return go<E, 1, TAIL>(p, grid, s);
-    case 2: return go<E, 2, TAIL>(p, grid, s);
-    case 3: return go<E, 3, TAIL>(p, grid, s);
-    case 4: return go<E, 4, TAIL>(p, grid, s);
-    case 5: return go<E, 5, TAIL>(p, grid, s);
-    default: return go<E, 6, TAIL>(p, grid, s);
+    case 0: return go<E, 0, TAIL, POLICY>(p, grid, s);
+    case 1: return go<E, 1, TAIL, POLICY>(p, grid, s);
+    case 2: return go<E, 2, TAIL, POLICY>(p, grid, s);
+    case 3: return go<E, 3, TAIL, POLICY>(p, grid, s);
+    case 4: return go<E, 4, TAIL, POLICY>(p, grid, s);
+    case 5: return go<E, 5, TAIL, POLICY>(p, grid, s);
+    default: return go<E, 6, TAIL, POLICY>(p, grid, s);
   }
+}
+template <class E>
+hipError_t by_layout(bool large, const NormParams& p, int grid, hipStream_t s) {
+  if (p.d % 8) return by_shape<E, true, 0>(p, grid, s);
+  return large ? by_shape<E, false, kLarge>(p, grid, s) : by_shape<E, false, 0>(p, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_norm_forward(bool bf16, const NormParams& p, int grid, hipStream_t s) {
+hipError_t launch_norm_forward(bool bf16, bool large, const NormParams& p, int grid, hipStream_t s) {
   if (grid <= 0) return hipSuccess;
-  if (bf16) return p.d % 8 ? by_shape<uint16_t, true>(p, grid, s) : by_shape<uint16_t, false>(p, grid, s);
-  return p.d % 8 ? by_shape<float, true>(p, grid, s) : by_shape<float, false>(p, grid, s);
+  return bf16 ? by_layout<uint16_t>(large, p, grid, s) : by_layout<float>(large, p, grid, s);
 }
 
 }  // namespace ge

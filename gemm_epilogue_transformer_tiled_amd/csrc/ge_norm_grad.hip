@@ -9,7 +9,9 @@
 namespace ge {
 namespace {
 
-template <class E, int TR, int V, bool TAIL, bool DROP>
+constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
+
+template <class E, int TR, int V, bool TAIL, bool DROP, int POLICY>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
   __shared__ float red[2][2][NT / 64];
@@ -24,28 +26,43 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dgain[i][j] = dbias[i][j] = 0.0f;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < p.rows; row += (int64_t)gridDim.x * RPW, turn ^= 1) {
-    Raw<E> rdy[V], rs[V], rds[V];
+  Raw<E> gain[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (p.gain) gain[i] = fetch<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
+  struct Row {
+    Raw<E> dy[V], s[V], ds[V];
+    float mean, rstd;
+  };
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  auto load = [&](Row& q, int64_t row) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = 8 * (t + TR * i);
-      rdy[i] = fetch<E, TAIL>((const E*)p.dy + row * p.lddy, col, d);
-      rs[i] = fetch<E, TAIL>((const E*)p.s + row * p.lds, col, d);
-      if (p.ds) rds[i] = fetch<E, TAIL>((const E*)p.ds + row * p.ldds, col, d);
+      q.dy[i] = fetch<E, TAIL, POLICY>((const E*)p.dy + row * p.lddy, col, d);
+      q.s[i] = fetch<E, TAIL, POLICY>((const E*)p.s + row * p.lds, col, d);
+      if (p.ds) q.ds[i] = fetch<E, TAIL, POLICY>((const E*)p.ds + row * p.ldds, col, d);
     }
-    const float mean = p.mean[row], rstd = p.rstd[row];
+    q.mean = p.mean[row];
+    q.rstd = p.rstd[row];
+  };
+  int turn = 0;
+  int64_t row = (int64_t)blockIdx.x * RPW + sub;
+  Row next{};
+  if (row < p.rows) load(next, row);
+  for (; row < p.rows; row += step, turn ^= 1) {
+    const Row q = next;
+    if (row + step < p.rows) load(next, row + step);   // on its way while this row is computed
+    const float mean = q.mean, rstd = q.rstd;
     float e[V][8], n[V][8], se = 0.0f, sen = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      Raw<E> g;
-      if (p.gain) g = fetch<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // (past the row's end dy is 0: whatever n is there, it adds nothing)
-        const float dy = get(rdy[i], j);
-        n[i][j] = (get(rs[i], j) - mean) * rstd;
-        e[i][j] = p.gain ? dy * get(g, j) : dy;
+        const float dy = get(q.dy[i], j);
+        n[i][j] = (get(q.s[i], j) - mean) * rstd;
+        e[i][j] = p.gain ? dy * get(gain[i], j) : dy;
         se += e[i][j];
         sen = fmaf(e[i][j], n[i][j], sen);
         dgain[i][j] = fmaf(dy, n[i][j], dgain[i][j]);
@@ -69,6 +86,15 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
       }
     }
     const float me = se / of_d, men = sen / of_d;
+    // The next row has landed before this one's stores go out: a wait for loads behind stores would wait for
+    // the stores too.
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      landed(next.dy[i]);
+      landed(next.s[i]);
+      landed(next.ds[i]);
+    }
+    asm volatile("" : "+v"(next.mean), "+v"(next.rstd));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = 8 * (t + TR * i);
@@ -76,16 +102,16 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         g[j] = rstd * fmaf(-n[i][j], men, e[i][j] - me);
-        if (p.ds) g[j] += get(rds[i], j);
+        if (p.ds) g[j] += get(q.ds[i], j);
       }
-      if (p.dr) put<E, TAIL>((E*)p.dr + row * p.lddr, col, d, rounded(g, E()));
+      if (p.dr) put<E, TAIL, POLICY>((E*)p.dr + row * p.lddr, col, d, rounded(g, E()));
       if (p.dx) {
         if constexpr (DROP) {
           const Words w = philox((uint32_t)row * blocks + (uint32_t)(t + TR * i), p.drop.site, key);
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[j] = dropped(g[j], w, j, p.drop);
         }
-        put<E, TAIL>((E*)p.dx + row * p.lddx, col, d, rounded(g, E()));
+        put<E, TAIL, POLICY>((E*)p.dx + row * p.lddx, col, d, rounded(g, E()));
       }
     }
   }
@@ -112,12 +138,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
     }
     if (sub == 0)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = 8 * (t + TR * i) + j;
-          if (col < d) out[which * d + col] = a[i][j];
-        }
+      for (int i = 0; i < V; ++i) put<float, TAIL>(out + which * d, 8 * (t + TR * i), d, rounded(a[i], float()));
   }
 }
 
@@ -147,33 +168,37 @@ __global__ __launch_bounds__(1024) void norm_sums(const float* part, int parts, 
   }
 }
 
-template <class E, int S, bool TAIL>
+template <class E, int S, bool TAIL, int POLICY>
 hipError_t go(const NormGradParams& p, int grid, hipStream_t s) {
-  constexpr int TR = kRowShape[S].threads, V = kRowShape[S].vecs;
+  constexpr int TR = kGradShape[S].threads, V = kGradShape[S].vecs;
   const dim3 g((unsigned)grid), b(TR < 256 ? 256 : TR);
-  if (p.drop.below) hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, true>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, false>), g, b, 0, s, p);
+  if (p.drop.below) hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, true, POLICY>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((norm_backward<E, TR, V, TAIL, false, POLICY>), g, b, 0, s, p);
   return hipGetLastError();
 }
-template <class E, bool TAIL>
+template <class E, bool TAIL, int POLICY>
 hipError_t by_shape(const NormGradParams& p, int grid, hipStream_t s) {
   switch (row_shape(p.d)) {
-    case 0: return go<E, 0, TAIL>(p, grid, s);
-    case 1: return go<E, 1, TAIL>(p, grid, s);
-    case 2: return go<E, 2, TAIL>(p, grid, s);
-    case 3: return go<E, 3, TAIL>(p, grid, s);
-    case 4: return go<E, 4, TAIL>(p, grid, s);
-    case 5: return go<E, 5, TAIL>(p, grid, s);
-    default: return go<E, 6, TAIL>(p, grid, s);
+    case 0: return go<E, 0, TAIL, POLICY>(p, grid, s);
+    case 1: return go<E, 1, TAIL, POLICY>(p, grid, s);
+    case 2: return go<E, 2, TAIL, POLICY>(p, grid, s);
+    case 3: return go<E, 3, TAIL, POLICY>(p, grid, s);
+    case 4: return go<E, 4, TAIL, POLICY>(p, grid, s);
+    case 5: return go<E, 5, TAIL, POLICY>(p, grid, s);
+    default: return go<E, 6, TAIL, POLICY>(p, grid, s);
   }
+}
+template <class E>
+hipError_t by_layout(bool large, const NormGradParams& p, int grid, hipStream_t s) {
+  if (p.d % 8) return by_shape<E, true, 0>(p, grid, s);
+  return large ? by_shape<E, false, kLarge>(p, grid, s) : by_shape<E, false, 0>(p, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_norm_backward(bool bf16, const NormGradParams& p, int grid, hipStream_t s) {
+hipError_t launch_norm_backward(bool bf16, bool large, const NormGradParams& p, int grid, hipStream_t s) {
   if (grid <= 0) return hipSuccess;
-  if (bf16) return p.d % 8 ? by_shape<uint16_t, true>(p, grid, s) : by_shape<uint16_t, false>(p, grid, s);
-  return p.d % 8 ? by_shape<float, true>(p, grid, s) : by_shape<float, false>(p, grid, s);
+  return bf16 ? by_layout<uint16_t>(large, p, grid, s) : by_layout<float>(large, p, grid, s);
 }
 
 hipError_t launch_norm_sums(const float* part, int parts, int d, float* dgain, float* dbias, hipStream_t s) {

@@ -15,6 +15,8 @@
 namespace ge {
 namespace {
 
+constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
+
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
@@ -46,7 +48,7 @@ __device__ __forceinline__ int code(float x, const Factor& q, float) {
   return (int)__builtin_rint((t + grid) - grid);
 }
 
-template <class E, int TR, int V, bool TAIL>
+template <class E, int TR, int V, bool TAIL, int POLICY>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR) void quant_rows(QuantParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
   __shared__ uint32_t top_of[2][NT / 64];
@@ -57,7 +59,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void quant_rows(QuantParams p)
     uint32_t top = 0;                                  // magnitudes compare like their bits, NaN above all
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      raw[i] = fetch<E, TAIL>((const E*)p.x + row * p.ldx, 8 * (t + TR * i), d);
+      raw[i] = fetch<E, TAIL, POLICY>((const E*)p.x + row * p.ldx, 8 * (t + TR * i), d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(get(raw[i], j)) & 0x7FFFFFFFu);
     }
@@ -84,7 +86,8 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void quant_rows(QuantParams p)
         for (int j = 0; j < 8; ++j) w[j >> 2] |= ((uint32_t)code(get(raw[i], j), q, E()) & 0xFFu) << (8 * (j & 3));
       if (!TAIL || col + 8 <= d) {
         typedef u32x2 Any8 __attribute__((aligned(1)));
-        *(Any8*)(out + col) = u32x2{w[0], w[1]};
+        if constexpr ((POLICY & kRowsStoresThrough) != 0) __builtin_nontemporal_store(u32x2{w[0], w[1]}, (Any8*)(out + col));
+        else *(Any8*)(out + col) = u32x2{w[0], w[1]};
       } else {
 #pragma unroll
         for (int j = 0; j < 7; ++j)
@@ -94,31 +97,36 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void quant_rows(QuantParams p)
   }
 }
 
-template <class E, int S, bool TAIL>
+template <class E, int S, bool TAIL, int POLICY>
 hipError_t go(const QuantParams& p, int grid, hipStream_t s) {
   constexpr int TR = kRowShape[S].threads, V = kRowShape[S].vecs;
-  hipLaunchKernelGGL((quant_rows<E, TR, V, TAIL>), dim3((unsigned)grid), dim3(TR < 256 ? 256 : TR), 0, s, p);
+  hipLaunchKernelGGL((quant_rows<E, TR, V, TAIL, POLICY>), dim3((unsigned)grid), dim3(TR < 256 ? 256 : TR), 0, s, p);
   return hipGetLastError();
 }
-template <class E, bool TAIL>
+template <class E, bool TAIL, int POLICY>
 hipError_t by_shape(const QuantParams& p, int grid, hipStream_t s) {
   switch (row_shape(p.d)) {
-    case 0: return go<E, 0, TAIL>(p, grid, s);
-    case 1: return go<E, 1, TAIL>(p, grid, s);
-    case 2: return go<E, 2, TAIL>(p, grid, s);
-    case 3: return go<E, 3, TAIL>(p, grid, s);
-    case 4: return go<E, 4, TAIL>(p, grid, s);
-    case 5: return go<E, 5, TAIL>(p, grid, s);
-    default: return go<E, 6, TAIL>(p, grid, s);
+    case 0: return go<E, 0, TAIL, POLICY>(p, grid, s);
+    case 1: return go<E, 1, TAIL, POLICY>(p, grid, s);
+    case 2: return go<E, 2, TAIL, POLICY>(p, grid, s);
+    case 3: return go<E, 3, TAIL, POLICY>(p, grid, s);
+    case 4: return go<E, 4, TAIL, POLICY>(p, grid, s);
+    case 5: return go<E, 5, TAIL, POLICY>(p, grid, s);
+    default: return go<E, 6, TAIL, POLICY>(p, grid, s);
   }
+}
+
+template <class E>
+hipError_t by_layout(bool large, const QuantParams& p, int grid, hipStream_t s) {
+  if (p.d % 8) return by_shape<E, true, 0>(p, grid, s);
+  return large ? by_shape<E, false, kLarge>(p, grid, s) : by_shape<E, false, 0>(p, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_quant(bool bf16, const QuantParams& p, int grid, hipStream_t s) {
+hipError_t launch_quant(bool bf16, bool large, const QuantParams& p, int grid, hipStream_t s) {
   if (grid <= 0) return hipSuccess;
-  if (bf16) return p.d % 8 ? by_shape<uint16_t, true>(p, grid, s) : by_shape<uint16_t, false>(p, grid, s);
-  return p.d % 8 ? by_shape<float, true>(p, grid, s) : by_shape<float, false>(p, grid, s);
+  return bf16 ? by_layout<uint16_t>(large, p, grid, s) : by_layout<float>(large, p, grid, s);
 }
 
 }  // namespace ge

@@ -58,30 +58,44 @@ __device__ __forceinline__ Raw<float> rounded(const float (&v)[8], float) {
   return r;
 }
 
+// Cache policy of a call's accesses (kRows*, ge_rows_internal.h).
+template <int POLICY>
+__device__ __forceinline__ u32x4 get16(const void* p) {
+  if constexpr ((POLICY & kRowsLoadsOnce) != 0) return __builtin_nontemporal_load((const Any16*)p);
+  else return *(const Any16*)p;
+}
+template <int POLICY>
+__device__ __forceinline__ void put16(void* p, u32x4 v) {
+  if constexpr ((POLICY & kRowsStoresThrough) != 0) __builtin_nontemporal_store(v, (Any16*)p);
+  else *(Any16*)p = v;
+}
+
 // Values col .. col + 7 of a row of d; zeros past its end.  TAIL: d is no multiple of eight, so the row's last
 // vector is read and written value by value.
-template <class E, bool TAIL>
+template <class E, bool TAIL, int POLICY = 0>
 __device__ __forceinline__ Raw<E> fetch(const E* row, int col, int d) {
   Raw<E> r = zero<E>();
   if (col + (TAIL ? 8 : 1) <= d) {
-    r.w = *(const Any16*)(row + col);
-    if constexpr (sizeof(E) == 4) r.w2 = *(const Any16*)(row + col + 4);
+    r.w = get16<POLICY>(row + col);
+    if constexpr (sizeof(E) == 4) r.w2 = get16<POLICY>(row + col + 4);
   } else if (TAIL && col < d) {
+    E v[7];                                            // all on their way before the first is waited for
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (col + j < d) {
-        if constexpr (sizeof(E) == 2) r.w[j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
-        else if (j < 4) r.w[j] = __float_as_uint(row[col + j]);
-        else r.w2[j - 4] = __float_as_uint(row[col + j]);
-      }
+    for (int j = 0; j < 7; ++j) v[j] = row[min(col + j, d - 1)];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      if constexpr (sizeof(E) == 2) r.w[j >> 1] |= col + j < d ? (uint32_t)v[j] << (16 * (j & 1)) : 0u;
+      else if (j < 4) r.w[j] = col + j < d ? __float_as_uint(v[j]) : 0u;
+      else r.w2[j - 4] = col + j < d ? __float_as_uint(v[j]) : 0u;
+    }
   }
   return r;
 }
-template <class E, bool TAIL>
+template <class E, bool TAIL, int POLICY = 0>
 __device__ __forceinline__ void put(E* row, int col, int d, const Raw<E>& r) {
   if (col + (TAIL ? 8 : 1) <= d) {
-    *(Any16*)(row + col) = r.w;
-    if constexpr (sizeof(E) == 4) *(Any16*)(row + col + 4) = r.w2;
+    put16<POLICY>(row + col, r.w);
+    if constexpr (sizeof(E) == 4) put16<POLICY>(row + col + 4, r.w2);
   } else if (TAIL && col < d) {
 #pragma unroll
     for (int j = 0; j < 7; ++j)
@@ -91,6 +105,10 @@ __device__ __forceinline__ void put(E* row, int col, int d, const Raw<E>& r) {
       }
   }
 }
+
+// Waits for a vector that was loaded earlier.
+__device__ __forceinline__ void landed(Raw<uint16_t>& r) { asm volatile("" : "+v"(r.w)); }
+__device__ __forceinline__ void landed(Raw<float>& r) { asm volatile("" : "+v"(r.w), "+v"(r.w2)); }
 
 // Sum over a wave, the same bits in every lane: exchanges within 16 lanes are DPP operands of the adds
 // (after the first two steps quads agree, so mirrored halves stand for the further ones).
@@ -130,10 +148,11 @@ struct Words {
 struct DropKey {
   uint32_t k0, k1, o0, o1;    // seed, offset (uniform)
 };
+// (through the scalar cache: no vector load waits for them)
 __device__ __forceinline__ DropKey drop_key(const DropParams& p) {
-  const uint32_t* q = (const uint32_t*)p.rng;
-  return DropKey{(uint32_t)__builtin_amdgcn_readfirstlane((int)q[0]), (uint32_t)__builtin_amdgcn_readfirstlane((int)q[1]),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)q[2]), (uint32_t)__builtin_amdgcn_readfirstlane((int)q[3])};
+  typedef const __attribute__((address_space(4))) uint32_t* Constant;
+  const Constant q = (Constant)(uintptr_t)p.rng;
+  return DropKey{q[0], q[1], q[2], q[3]};
 }
 __device__ __forceinline__ Words philox(uint32_t block, uint32_t site, const DropKey& key) {
   uint32_t c0 = block, c1 = site, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;

@@ -32,6 +32,7 @@ struct ge_i8_plan {
   ge_i8_desc_t desc;
   int device;
   int tile, splits;           // ge::FfnTile
+  bool few;                   // the few-row kernel instead of a tile
 };
 
 namespace {
@@ -106,9 +107,12 @@ int even_grid(int64_t turns, int64_t most) {
   return turns > 0 ? (int)ceil_div(turns, ceil_div(turns, most)) : 0;
 }
 // Workgroups that fit `waves` waves on every compute unit.
-int64_t resident(int shape, int64_t waves) {
-  return 256 * std::max<int64_t>(1, waves * 64 / std::max(ge::kRowShape[shape].threads, 256));
+int64_t resident(const ge::RowShape& s, int64_t waves) {
+  return 256 * std::max<int64_t>(1, waves * 64 / std::max(s.threads, 256));
 }
+
+// Whether a call's outputs pass what the caches would keep of them for the next one.
+bool large(int64_t rows, int64_t d, int64_t size, int outputs) { return rows * d * size * outputs > ge::kRowsLarge; }
 
 hipStream_t stream_of(void* s) { return static_cast<hipStream_t>(s); }
 ge_status_t status_of(hipError_t e) { return e == hipSuccess ? GE_OK : GE_ERR_HIP; }
@@ -160,9 +164,9 @@ ge_status_t ge_norm_create(const ge_norm_desc_t* d, ge_norm_handle_t* handle) {
   if (st != GE_OK) return st;
   p->desc = *d;
   const int shape = ge::row_shape(d->d);
-  const int64_t groups = ceil_div(d->rows, ge::rows_at_once(shape));
-  p->grid_forward = even_grid(groups, resident(shape, 32));
-  p->grid_backward = even_grid(groups, resident(shape, 16));
+  const ge::RowShape &fwd = ge::kRowShape[shape], &bwd = ge::kGradShape[shape];
+  p->grid_forward = (int)std::min<int64_t>(ceil_div(d->rows, ge::rows_at_once(fwd)), 1 << 20);
+  p->grid_backward = even_grid(ceil_div(d->rows, ge::rows_at_once(bwd)), resident(bwd, 16));
   return GE_OK;
 }
 
@@ -200,7 +204,7 @@ ge_status_t ge_norm_forward(ge_norm_handle_t h, const ge_norm_args_t* a, void* s
   p.rows = d.rows; p.ldx = d.ldx; p.ldr = d.ldr; p.lds = d.lds; p.ldy = d.ldy;
   p.d = (int32_t)d.d;
   p.eps = d.eps;
-  return status_of(ge::launch_norm_forward(d.dtype == GE_DT_BF16, p, h->grid_forward, stream_of(stream)));
+  return status_of(ge::launch_norm_forward(d.dtype == GE_DT_BF16, large(d.rows, d.d, size, a->S ? 2 : 1), p, h->grid_forward, stream_of(stream)));
 }
 
 ge_status_t ge_norm_backward(ge_norm_handle_t h, const ge_norm_args_t* a, void* stream) {
@@ -240,7 +244,8 @@ ge_status_t ge_norm_backward(ge_norm_handle_t h, const ge_norm_args_t* a, void* 
   if (!drop) p.drop.below = 0;
   p.rows = d.rows; p.lddy = d.lddy; p.lds = d.lds; p.ldds = d.ldds; p.lddx = d.lddx; p.lddr = d.lddr;
   p.d = (int32_t)d.d;
-  if (ge::launch_norm_backward(d.dtype == GE_DT_BF16, p, h->grid_backward, s) != hipSuccess) return GE_ERR_HIP;
+  const int outputs = (a->dX != nullptr) + (a->dR != nullptr);
+  if (ge::launch_norm_backward(d.dtype == GE_DT_BF16, large(d.rows, d.d, size, outputs), p, h->grid_backward, s) != hipSuccess) return GE_ERR_HIP;
   if (!sums) return GE_OK;
   return status_of(ge::launch_norm_sums(part, h->grid_backward, p.d, a->dgain, a->dbias, s));
 }
@@ -292,7 +297,7 @@ ge_status_t run_dropout(const ge_dropout_plan* h, const void* x, int64_t ldx, co
   p.drop = drop_params(d.p, d.site, rng);
   p.rows = d.rows; p.ldx = ldx; p.ldr = ldr; p.ldy = ldy;
   p.d = (int32_t)d.d;
-  return status_of(ge::launch_dropout(d.dtype == GE_DT_BF16, p, stream_of(stream)));
+  return status_of(ge::launch_dropout(d.dtype == GE_DT_BF16, large(d.rows, d.d, size, 1), p, stream_of(stream)));
 }
 }  // namespace
 
@@ -330,7 +335,7 @@ ge_status_t ge_quant_create(const ge_quant_desc_t* d, ge_quant_handle_t* handle)
   st = make(&p, handle);
   if (st != GE_OK) return st;
   p->desc = *d;
-  const int shape = ge::row_shape(d->d);
+  const ge::RowShape& shape = ge::kRowShape[ge::row_shape(d->d)];
   p->grid = even_grid(ceil_div(d->rows, ge::rows_at_once(shape)), resident(shape, 32));
   return GE_OK;
 }
@@ -352,7 +357,7 @@ ge_status_t ge_quant_run(ge_quant_handle_t h, const ge_quant_args_t* a, void* st
   p.x = a->X; p.codes = a->codes; p.scale = a->scale;
   p.rows = d.rows; p.ldx = d.ldx; p.ldq = d.ldq;
   p.d = (int32_t)d.d;
-  return status_of(ge::launch_quant(d.dtype == GE_DT_BF16, p, h->grid, stream_of(stream)));
+  return status_of(ge::launch_quant(d.dtype == GE_DT_BF16, large(d.rows, d.d, 1, 1), p, h->grid, stream_of(stream)));
 }
 
 }  // extern "C"
@@ -378,31 +383,41 @@ bool grid_fits(int tile, int64_t M, int64_t N) {
   return (double)ceil_div(M, ti.bm) * (double)ceil_div(N, ti.bn) * (tile == ge::FFN_T64 ? 256 : 512) <= 4294967295.0;
 }
 
+// Whether the few-row kernel takes the product: the tokens' codes fit a workgroup's LDS, and several workgroups
+// fit a compute unit, unless there are no more of them than units.  (17 tokens at 11008 x 4096, 70 KB: 16.0 us in both;
+// 27 tokens, 111 KB: 21.4 against 16.3 in tiles, but 8.4 against 9.4 at 4096 x 4096, 256 workgroups.)
+bool few_rows(const ge_i8_desc_t& d) {
+  if (d.tile || d.M > ge::kI8FewRows) return false;
+  const int64_t lds = ge::i8_few_lds(d.M, d.K);
+  return lds <= (ceil_div(d.N, ge::kI8FewCols) <= 256 ? ge::kI8FewLds : ge::kI8FewLds / 2);
+}
+
 // Tile and splits: the least estimated time in microseconds.  A tile costs `fixed` and `slot` for every 128
 // codes of the contraction, `crowd` instead where workgroups share a compute unit or come in rounds; a
-// split adds the partial sums' way through memory and back.  The figures need only rank the choices.
+// split adds a ticket, the last workgroup's reads and the partial sums' way through memory and back.  The
+// figures were measured over 27 to 8192 tokens and 4 to 86 slots; they need only rank the choices.
 void pick(ge_i8_plan* p) {
   const ge_i8_desc_t& d = p->desc;
-  p->tile = ge::FFN_T256;
+  p->tile = d.tile ? d.tile - 1 : (int)ge::FFN_T256;
   p->splits = 1;
-  if (d.tile) {
-    p->tile = d.tile - 1;
-    return;
-  }
+  p->few = few_rows(d);
+  if (d.tile || p->few) return;
   const int64_t slots = ceil_div(d.K, 128);
   struct Cost { double fixed, slot, crowd; };
-  const Cost cost[ge::FFN_TILES] = {{7.0, 1.3, 1.4}, {3.0, 0.5, 0.57}, {1.5, 0.26, 0.21}};
+  const Cost cost[ge::FFN_TILES] = {{7.0, 1.0, 1.35}, {3.5, 0.4, 0.57}, {3.0, 0.25, 0.21}};
   double least = 1e300;
   for (int t = 0; t < ge::FFN_TILES; ++t) {
     if (!grid_fits(t, d.M, d.N)) continue;
     const ge::FfnTileInfo ti = ge::ffn_tile_info(t);
-    const double tiles = (double)ceil_div(d.M, ti.bm) * (double)ceil_div(d.N, ti.bn);
-    for (int s = 1; s <= (t == ge::FFN_T256 ? 1 : kMaxSplits); s *= 2) {
-      if (s > 1 && (slots < 4 * s || tiles * s > ge::kFfnMaxSplitGroups)) break;
+    const int64_t tiles_m = ceil_div(d.M, ti.bm);
+    const double tiles = (double)tiles_m * (double)ceil_div(d.N, ti.bn);
+    for (int s = 1; s <= (t == ge::FFN_T256 ? 1 : kMaxSplits); ++s) {
+      if (s > 1 && (slots < 2 * s || tiles * s > ge::kFfnMaxSplitGroups)) break;
       const double ratio = tiles * s / 256.0, rounds = ratio < 4.0 ? std::ceil(ratio) : ratio;
       const double mine = (double)ceil_div(slots, s);
       double us = rounds > 1.0 ? rounds * (cost[t].fixed + mine * cost[t].crowd) : cost[t].fixed + mine * cost[t].slot;
-      if (s > 1) us += 2.5 + tiles * s * ti.bm * ti.bn * 8.0 / 3e6;
+      const double rows = (double)std::min<int64_t>(ceil_div(d.M, 16) * 16, tiles_m * ti.bm);
+      if (s > 1) us += 1.5 + 0.3 * s + rows * (double)ceil_div(d.N, ti.bn) * ti.bn * s * 4.0 * 0.9e-6;
       if (us < least) {
         least = us;
         p->tile = t;
@@ -464,7 +479,8 @@ ge_status_t ge_i8_workspace_size(ge_i8_handle_t h, size_t* bytes) {
 ge_status_t ge_i8_describe(ge_i8_handle_t h, char* buf, size_t len) {
   if (!h || !buf || len == 0) return GE_ERR_INVALID_ARG;
   const int rows[] = {256, 128, 64};
-  std::snprintf(buf, len, "tile=%d splits=%d act=%d", rows[h->tile], h->splits, (int)h->desc.act);
+  if (h->few) std::snprintf(buf, len, "few rows act=%d", (int)h->desc.act);
+  else std::snprintf(buf, len, "tile=%d splits=%d act=%d", rows[h->tile], h->splits, (int)h->desc.act);
   return GE_OK;
 }
 
@@ -485,6 +501,12 @@ ge_status_t ge_i8_run(ge_i8_handle_t h, const ge_i8_args_t* a, void* stream) {
   b.write({a->workspace, 1, bytes, bytes, 1}, 16);
   if (!b.apart(same) || (bytes > 0 && a->workspace_bytes < (size_t)bytes)) return GE_ERR_INVALID_ARG;
   if (!ge::block::is_current(h->device)) return GE_ERR_DEVICE;
+  const ge::I8Epilogue ep{a->x_scale, a->w_scale, d.bias ? a->bias : nullptr, d.act, d.dtype == GE_DT_FP32};
+  if (h->few) {
+    const ge::I8Few f{a->X, a->W, d.residual ? a->residual : nullptr, a->Y, ep, d.ldx, d.ldw, d.ldy, d.ldr,
+                      (int32_t)d.M, (int32_t)d.N, (int32_t)d.K, (int32_t)ge::i8_few_pitch(d.K)};
+    return status_of(ge::launch_i8_few(f, stream_of(stream)));
+  }
   const ge::FfnTileInfo ti = ge::ffn_tile_info(h->tile);
   ge::I8Launch l{};
   ge::FfnProduct& p = l.prod[0];
@@ -503,7 +525,7 @@ ge_status_t ge_i8_run(ge_i8_handle_t h, const ge_i8_args_t* a, void* stream) {
     l.ctr = static_cast<uint32_t*>(a->workspace);
     l.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a->workspace) + ge::kTicketBytes);
   }
-  l.ep = ge::I8Epilogue{a->x_scale, a->w_scale, d.bias ? a->bias : nullptr, d.act, d.dtype == GE_DT_FP32};
+  l.ep = ep;
   return status_of(ge::launch_i8(h->tile, l, stream_of(stream)));
 }
 

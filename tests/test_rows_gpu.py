@@ -382,7 +382,8 @@ def run_i8(X, W, xs, ws, b, R, act, dtype, tile=None, pads=(0, 0, 0, 0)):
 
 
 I8_SIZES = [(1, 8, 16), (1, 128, 128), (3, 136, 48), (16, 256, 4096), (17, 1000, 272), (64, 64, 64), (65, 72, 144), (129, 520, 1040),
-            (256, 256, 256), (300, 776, 2064), (777, 264, 528), (1, 4096, 1040), (16, 1032, 11008), (1000, 2056, 144)]
+            (256, 256, 256), (300, 776, 2064), (777, 264, 528), (1, 4096, 1040), (16, 1032, 11008), (1000, 2056, 144), (2, 24, 11008), (13, 264, 11008),
+            (27, 520, 4112), (32, 1000, 4096), (19, 4200, 4096), (32, 16, 496), (33, 136, 2048), (5, 72, 131056)]
 
 
 @pytest.mark.parametrize("tile", [None, rows.GE_I8_TILE_256, rows.GE_I8_TILE_128, rows.GE_I8_TILE_64])
