@@ -23,10 +23,12 @@ __global__ __launch_bounds__(kThreads) void dropout(DropoutParams p) {
     const E* x = (const E*)p.x + (FLAT ? 8 * i : (int64_t)row * p.ldx);
     const E* r = (const E*)p.r + (FLAT ? 8 * i : (int64_t)row * p.ldr);
     E* y = (E*)p.y + (FLAT ? 8 * i : (int64_t)row * p.ldy);
-    const Raw<E> rx = fetch<E, TAIL, POLICY>(x, col, d);
+    Raw<E> rx = fetch<E, TAIL, POLICY>(x, col, d);
     Raw<E> rr;
     if constexpr (RES) rr = fetch<E, TAIL, POLICY>(r, col, d);
     const Words w = philox(b, p.drop.site, key);
+    settle<TAIL>(rx, col, d);
+    if constexpr (RES) settle<TAIL>(rr, col, d);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

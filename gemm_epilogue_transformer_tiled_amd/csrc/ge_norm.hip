@@ -32,6 +32,8 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      settle<TAIL>(raw[i], 8 * (t + TR * i), d);
+      if (p.r) settle<TAIL>(rr[i], 8 * (t + TR * i), d);
       Words w{};
       if constexpr (DROP) w = philox((uint32_t)row * blocks + (uint32_t)(t + TR * i), p.drop.site, key);
 #pragma unroll
@@ -69,12 +71,12 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
       if (p.gain) {
-        const Raw<E> g = fetch<E, TAIL>((const E*)p.gain, col, d);
+        const Raw<E> g = fetch_settled<E, TAIL>((const E*)p.gain, col, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= get(g, j);
       }
       if (p.bias) {
-        const Raw<E> b = fetch<E, TAIL>((const E*)p.bias, col, d);
+        const Raw<E> b = fetch_settled<E, TAIL>((const E*)p.bias, col, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += get(b, j);
       }

@@ -29,7 +29,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
   Raw<E> gain[V];
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (p.gain) gain[i] = fetch<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
+    if (p.gain) gain[i] = fetch_settled<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
   struct Row {
     Raw<E> dy[V], s[V], ds[V];
     float mean, rstd;
@@ -51,8 +51,14 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
   Row next{};
   if (row < p.rows) load(next, row);
   for (; row < p.rows; row += step, turn ^= 1) {
-    const Row q = next;
+    Row q = next;
     if (row + step < p.rows) load(next, row + step);   // on its way while this row is computed
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      settle<TAIL>(q.dy[i], 8 * (t + TR * i), d);
+      settle<TAIL>(q.s[i], 8 * (t + TR * i), d);
+      if (p.ds) settle<TAIL>(q.ds[i], 8 * (t + TR * i), d);
+    }
     const float mean = q.mean, rstd = q.rstd;
     float e[V][8], n[V][8], se = 0.0f, sen = 0.0f;
 #pragma unroll

@@ -60,6 +60,10 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void quant_rows(QuantParams p)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       raw[i] = fetch<E, TAIL, POLICY>((const E*)p.x + row * p.ldx, 8 * (t + TR * i), d);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      settle<TAIL>(raw[i], 8 * (t + TR * i), d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(get(raw[i], j)) & 0x7FFFFFFFu);
     }

@@ -70,39 +70,83 @@ __device__ __forceinline__ void put16(void* p, u32x4 v) {
   else *(Any16*)p = v;
 }
 
-// Values col .. col + 7 of a row of d; zeros past its end.  TAIL: d is no multiple of eight, so the row's last
-// vector is read and written value by value.
+// Values col .. col + 7 of a row of d, zeros past its end.  TAIL: d is no multiple of eight.  The row's last vector is
+// then loaded from its last eight values, and settle() shifts them to their places when they are used: nothing
+// waits for a load when it is made.  (Value by value, and put together at once, the last vector held up its whole row:
+// norm of 16432 x 1021 bf16 30.7 us and its gradient 63.4.)
 template <class E, bool TAIL, int POLICY = 0>
 __device__ __forceinline__ Raw<E> fetch(const E* row, int col, int d) {
   Raw<E> r = zero<E>();
-  if (col + (TAIL ? 8 : 1) <= d) {
-    r.w = get16<POLICY>(row + col);
-    if constexpr (sizeof(E) == 4) r.w2 = get16<POLICY>(row + col + 4);
-  } else if (TAIL && col < d) {
-    E v[7];                                            // all on their way before the first is waited for
-#pragma unroll
-    for (int j = 0; j < 7; ++j) v[j] = row[min(col + j, d - 1)];
+  if (col >= d) return r;
+  if (!TAIL || d >= 8) {                               // (uniform)
+    const E* at = row + (TAIL ? min(col, d - 8) : col);
+    r.w = get16<POLICY>(at);
+    if constexpr (sizeof(E) == 4) r.w2 = get16<POLICY>(at + 4);
+  } else {
 #pragma unroll
     for (int j = 0; j < 7; ++j) {
-      if constexpr (sizeof(E) == 2) r.w[j >> 1] |= col + j < d ? (uint32_t)v[j] << (16 * (j & 1)) : 0u;
-      else if (j < 4) r.w[j] = col + j < d ? __float_as_uint(v[j]) : 0u;
-      else r.w2[j - 4] = col + j < d ? __float_as_uint(v[j]) : 0u;
+      const E v = row[min(j, d - 1)];
+      if constexpr (sizeof(E) == 2) r.w[j >> 1] |= j < d ? (uint32_t)v << (16 * (j & 1)) : 0u;
+      else if (j < 4) r.w[j] = j < d ? __float_as_uint(v) : 0u;
+      else r.w2[j - 4] = j < d ? __float_as_uint(v) : 0u;
     }
   }
   return r;
 }
+template <bool TAIL>
+__device__ __forceinline__ void settle(Raw<uint16_t>& r, int col, int d) {
+  if (!TAIL || d < 8 || col >= d || col + 8 <= d) return;
+  const int s = 16 * (8 - (d & 7));                    // bits; uniform
+  uint64_t lo64 = (uint64_t)r.w[1] << 32 | r.w[0], hi64 = (uint64_t)r.w[3] << 32 | r.w[2];
+  lo64 = s < 64 ? lo64 >> s | hi64 << (64 - s) : hi64 >> (s - 64);
+  hi64 = s < 64 ? hi64 >> s : 0;
+  r.w = u32x4{(uint32_t)lo64, (uint32_t)(lo64 >> 32), (uint32_t)hi64, (uint32_t)(hi64 >> 32)};
+}
+template <bool TAIL>
+__device__ __forceinline__ void settle(Raw<float>& r, int col, int d) {
+  if (!TAIL || d < 8 || col >= d || col + 8 <= d) return;
+  const int s = 8 - (d & 7);                           // values; uniform
+  if (s & 1) {
+    r.w = u32x4{r.w[1], r.w[2], r.w[3], r.w2[0]};
+    r.w2 = u32x4{r.w2[1], r.w2[2], r.w2[3], 0};
+  }
+  if (s & 2) {
+    r.w = u32x4{r.w[2], r.w[3], r.w2[0], r.w2[1]};
+    r.w2 = u32x4{r.w2[2], r.w2[3], 0, 0};
+  }
+  if (s & 4) {
+    r.w = r.w2;
+    r.w2 = u32x4{0, 0, 0, 0};
+  }
+}
+template <class E, bool TAIL>
+__device__ __forceinline__ Raw<E> fetch_settled(const E* row, int col, int d) {
+  Raw<E> r = fetch<E, TAIL>(row, col, d);
+  settle<TAIL>(r, col, d);
+  return r;
+}
+// The last vector of a ragged row goes out in runs of four, two and one.
 template <class E, bool TAIL, int POLICY = 0>
 __device__ __forceinline__ void put(E* row, int col, int d, const Raw<E>& r) {
+  typedef u32x2 Any8 __attribute__((aligned(2)));
+  typedef uint32_t Any4 __attribute__((aligned(2)));
   if (col + (TAIL ? 8 : 1) <= d) {
     put16<POLICY>(row + col, r.w);
     if constexpr (sizeof(E) == 4) put16<POLICY>(row + col + 4, r.w2);
   } else if (TAIL && col < d) {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (col + j < d) {
-        if constexpr (sizeof(E) == 2) row[col + j] = (uint16_t)(r.w[j >> 1] >> (16 * (j & 1)));
-        else row[col + j] = get(r, j);
-      }
+    const int n = d & 7;                               // uniform
+    E* at = row + col;
+    if constexpr (sizeof(E) == 2) {
+      if (n & 4) *(Any8*)at = u32x2{r.w[0], r.w[1]};
+      const uint32_t a = (n & 4) ? r.w[2] : r.w[0], b = (n & 4) ? r.w[3] : r.w[1];
+      if (n & 2) *(Any4*)(at + (n & 4)) = a;
+      if (n & 1) at[n & 6] = (uint16_t)((n & 2) ? b : a);
+    } else {
+      if (n & 4) *(Any16*)at = r.w;
+      const u32x4 a = (n & 4) ? r.w2 : r.w;
+      if (n & 2) *(Any8*)(at + (n & 4)) = u32x2{a[0], a[1]};
+      if (n & 1) at[n & 6] = __uint_as_float((n & 2) ? a[2] : a[0]);
+    }
   }
 }
 
