@@ -8,11 +8,14 @@ namespace ge {
 // ---- how a row lies on threads ----
 // Eight values are a vector; thread t of a row's `threads` holds vectors t, t + threads, ... up to `vecs`
 // of them.  So a wave reads 1 KB of bf16 at a time, and the whole row is in registers between its
-// sums and its outputs.
+// sums and its outputs.  More threads with fewer vectors each are slower (norm of 65536 x 1024 bf16 90
+// us, with four times the threads 113; codes 39 against 52; 4096 x 16384 with 512 threads 91, with 1024 98),
+// but for few rows (16 x 11008 with 512 threads 5.6 us, with 1024 5.0).
 struct RowShape { int threads, vecs; };
 constexpr int kRowShapes = 7;
-constexpr RowShape kRowShape[kRowShapes] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2}, {1024, 2}, {1024, 4}};
-// The backward pass holds the sums of its columns too: more threads for a row.
+constexpr RowShape kRowShape[kRowShapes] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2}, {512, 4}, {1024, 4}};
+// The backward pass holds the sums of its columns too: more threads for a row (16384 x 4096 bf16 with 512 threads
+// 114 us, with 256 124).
 constexpr RowShape kGradShape[kRowShapes] = {{64, 1}, {64, 2}, {256, 1}, {512, 1}, {1024, 1}, {1024, 2}, {1024, 4}};
 constexpr int64_t kRowMax = 8 * 1024 * 4;
 // The same widths in both tables: 512, 1024, 2048, ... 32768.
@@ -24,7 +27,9 @@ inline int row_shape(int64_t d) {
 // Rows a workgroup takes at a time: workgroups have 256 threads at least.
 inline int rows_at_once(const RowShape& s) { return s.threads < 256 ? 256 / s.threads : 1; }
 
-// Cache policy of large calls (past kRowsLarge bytes of outputs; ragged rows keep the default).
+// Cache policy of large calls (past kRowsLarge bytes of outputs; ragged rows keep the default): nothing of them would
+// be left in the caches for the next call, so their loads and stores do not push other lines out, nor wait for
+// room (16384 x 4096 bf16, 134 MB an array: norm 90 us against 100, its gradient 124 against 131).
 enum RowsPolicy : int { kRowsLoadsOnce = 1, kRowsStoresThrough = 2 };
 constexpr int64_t kRowsLarge = int64_t(64) << 20;
 

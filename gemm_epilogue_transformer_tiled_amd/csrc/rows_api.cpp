@@ -166,7 +166,10 @@ ge_status_t ge_norm_create(const ge_norm_desc_t* d, ge_norm_handle_t* handle) {
   const int shape = ge::row_shape(d->d);
   const ge::RowShape &fwd = ge::kRowShape[shape], &bwd = ge::kGradShape[shape];
   p->grid_forward = (int)std::min<int64_t>(ceil_div(d->rows, ge::rows_at_once(fwd)), 1 << 20);
-  p->grid_backward = even_grid(ceil_div(d->rows, ge::rows_at_once(bwd)), resident(bwd, 16));
+  // Eight waves on a compute unit, though more would fit: a workgroup leaves 8 d bytes of partial sums, and each row's
+  // loads are ahead of it anyhow (16384 x 4096 bf16 112.8 us against 125.9 with 16 waves, x 2048 63.4 against 71.0; 4
+  // waves 83).
+  p->grid_backward = even_grid(ceil_div(d->rows, ge::rows_at_once(bwd)), resident(bwd, 8));
   return GE_OK;
 }
 
@@ -386,6 +389,7 @@ bool grid_fits(int tile, int64_t M, int64_t N) {
 // Whether the few-row kernel takes the product: the tokens' codes fit a workgroup's LDS, and several workgroups
 // fit a compute unit, unless there are no more of them than units.  (17 tokens at 11008 x 4096, 70 KB: 16.0 us in both;
 // 27 tokens, 111 KB: 21.4 against 16.3 in tiles, but 8.4 against 9.4 at 4096 x 4096, 256 workgroups.)
+// (Fewer than 2^22 outputs a token, the most that a pitch allows: the launch's threads fit 32 bits.)
 bool few_rows(const ge_i8_desc_t& d) {
   if (d.tile || d.M > ge::kI8FewRows) return false;
   const int64_t lds = ge::i8_few_lds(d.M, d.K);

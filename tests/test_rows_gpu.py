@@ -124,6 +124,30 @@ def test_norm_with_dropout_and_residual(M, d, pad, residual, p, dtype):
         assert all(canary_ok(t) for t in (S, Y, dX, dR))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d", [8200, 11008, 16383, 16392, 32767, 32768])
+def test_norm_backward_of_many_wide_rows(d, dtype):
+    """Several rows a workgroup, with everything a call can have and over its inputs."""
+    M = 600
+    gen = torch.Generator("cuda").manual_seed(d)
+    S, dY, dS, gain = (normal(gen, (M, d), dtype, 2.0, 0.5), normal(gen, (M, d), dtype, 0.05), normal(gen, (M, d), dtype, 0.05),
+                       normal(gen, (d,), dtype, 0.2, 1.0))
+    x = S.double()
+    mean, rstd = x.mean(1).float(), (1 / torch.sqrt(x.var(1, correction=0) + 1e-5)).float()
+    del x
+    plan = rows.LayerNorm(M, d, dtype=dtype, residual=True, dropout=0.25, site=SITE)
+    for g, add in ((gain, dS), (None, None)):
+        f = factors_of(M, d, 0.25)
+        ref, tol = rp.norm_backward(dY, S, add, mean, rstd, g, f)
+        dX, dgain, dbias = dY.clone(), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+        dR = dS.clone() if add is not None else torch.empty_like(dY)
+        plan.backward(rows.make_norm_args(S=S, mean=mean, rstd=rstd, gain=g, rng=rng_of(), dY=dX, dS=dR if add is not None else None,
+                                          dX=dX, dR=dR, dgain=dgain, dbias=dbias))
+        for n, got in (("dX", dX), ("dR", dR), ("dgain", dgain), ("dbias", dbias)):
+            rp.check(got, ref[n], tol[n], (n, d))
+        del f, ref, tol
+
+
 def test_norm_optional_outputs_and_in_place():
     """Every subset of outputs gives the same bits; S over R, Y over X, dX over dY, dR over dS."""
     M, d = 70, 520
