@@ -13,8 +13,16 @@ namespace {
 
 constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
 
+// Waves that the registers have to leave room for on a SIMD: two workgroups of 512 threads a compute unit, and
+// six of 256 with bf16 rows, where ragged rows would take a few registers more (8192 x 11007 bf16 with dropout 247 us against
+// 289, 8192 x 2051 38 against 42; more waves than these spill).
+template <class E>
+constexpr int waves_of(int threads, int vecs) {
+  return threads == 512 && vecs > 2 ? 4 : threads == 256 && vecs == 2 && sizeof(E) == 2 ? 6 : 1;
+}
+
 template <class E, int TR, int V, bool TAIL, bool DROP, int POLICY>
-__global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_forward(NormParams p) {
+__global__ __launch_bounds__(TR < 256 ? 256 : TR, waves_of<E>(TR, V)) void norm_forward(NormParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
   __shared__ float red[2][NT / 64];
   const int t = (int)threadIdx.x % TR, sub = (int)threadIdx.x / TR, d = p.d;
