@@ -20,7 +20,7 @@
  * workspaces of their own, and clear a workspace again after a call that did not complete.
  *
  * Rows: every matrix is row-major, its leading dimension in elements.  Elements between a row's
- * length and its leading dimension are neither read nor written.  Outputs must not overlap inputs or
+ * length and its leading dimension are not written, and nothing depends on them.  Outputs must not overlap inputs or
  * each other, except where an operator says that an output may be an input itself (same pointer and
  * leading dimension).
  *
