@@ -1,7 +1,7 @@
 // Product of int8 codes, few rows (decoding): one pass over the weights (gfx950).
 //
 // With few rows what bounds the product is how many of the weights' bytes are in flight.  A workgroup takes 16
-// columns (weight rows) and all of K, which its eight waves split; their int32 sums meet in LDS, so there
+// columns (weight rows), or 8 where that spreads better, and all of K, which its eight waves split; their int32 sums meet in LDS, so there
 // are no partial sums in memory, no tickets and no workspace.  A wave loads the weights straight into
 // registers, 512 codes of all 16 rows at a time (eight loads, whole cache lines), and multiplies them with the
 // tokens' codes by v_mfma_i32_16x16x64_i8; lane l holds 16 codes, 16 (l / 16) .. + 15 of 64, of weight row
@@ -18,7 +18,7 @@ namespace ge {
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-constexpr int kWaves = kI8FewWaves, kCols = kI8FewCols, kUnits = kI8FewStep / 128;
+constexpr int kWaves = kI8FewWaves, kUnits = kI8FewStep / 128;
 
 // RB: blocks of 16 tokens.
 template <int RB>
@@ -29,8 +29,8 @@ __global__ __launch_bounds__(64 * kWaves) void i8_few(I8Few p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t l16 = (uint32_t)(lane & 15), q16 = (uint32_t)(lane >> 4);
-  const int n0 = (int)blockIdx.x * kCols, K = p.K, M = p.M;
-  const int ncols = min(p.N - n0, kCols);
+  const int n0 = (int)blockIdx.x * p.cols, K = p.K, M = p.M;
+  const int ncols = min(p.N - n0, p.cols);
 
   // ---- what the outputs need besides the sums: thread t ends columns 4 (t % 4) .. + 3 of row t / 4 ----
   const int row = tid / 4, col = 4 * (tid % 4);
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_few(I8Few p) {
 hipError_t launch_i8_few(const I8Few& p, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   if (p.M > kI8FewRows || i8_few_lds(p.M, p.K) > kI8FewLds) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((p.N + kCols - 1) / kCols)), block(64 * kWaves);
+  const dim3 grid((unsigned)((p.N + p.cols - 1) / p.cols)), block(64 * kWaves);
   const unsigned bytes = (unsigned)i8_few_lds(p.M, p.K);
   if (p.M <= 16) hipLaunchKernelGGL(i8_few<1>, grid, block, bytes, s, p);
   else hipLaunchKernelGGL(i8_few<2>, grid, block, bytes, s, p);

@@ -94,6 +94,7 @@ struct I8Few {
   int64_t ldx, ldw, ldy, ldr;
   int32_t M, N, K;
   int32_t x_pitch;            // bytes between the tokens' codes in LDS
+  int32_t cols;               // of a workgroup: kI8FewCols or half of them
 };
 constexpr int kI8FewRows = 32, kI8FewCols = 16, kI8FewWaves = 8;
 constexpr int kI8FewStep = 512;               // codes of K a wave takes at a time

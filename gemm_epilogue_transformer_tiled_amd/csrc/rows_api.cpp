@@ -33,6 +33,7 @@ struct ge_i8_plan {
   int device;
   int tile, splits;           // ge::FfnTile
   bool few;                   // the few-row kernel instead of a tile
+  int32_t cols;               // its columns a workgroup
 };
 
 namespace {
@@ -396,6 +397,15 @@ bool few_rows(const ge_i8_desc_t& d) {
   return lds <= (ceil_div(d.N, ge::kI8FewCols) <= 256 ? ge::kI8FewLds : ge::kI8FewLds / 2);
 }
 
+// Columns of its workgroups: half as many where each workgroup then still has a compute unit to itself (one token: 264 x 11008
+// 7.6 -> 5.9 us, 2048 x 8192 6.6 -> 6.1; 3000 x 4000, past it, would take 5.1 against 4.7), and for few tokens where some
+// compute units would have two workgroups of whole width and the others one (4608 x 4096 7.8 -> 6.9, 6144 x 4096 8.7 -> 8.2;
+// with 16 tokens 5120 x 5120 would take 15 us against 13, and from 512 workgroups on, 8192 x 8192, one token 16.5 against 15.2).
+int few_cols(const ge_i8_desc_t& d) {
+  const int64_t groups = ceil_div(d.N, ge::kI8FewCols);
+  return groups <= 128 || (d.M <= 4 && groups > 256 && groups <= 384) ? ge::kI8FewCols / 2 : ge::kI8FewCols;
+}
+
 // Tile and splits: the least estimated time in microseconds.  A tile costs `fixed` and `slot` for every 128
 // codes of the contraction, `crowd` instead where workgroups share a compute unit or come in rounds; a
 // split adds a ticket, the last workgroup's reads and the partial sums' way through memory and back.  The
@@ -405,6 +415,7 @@ void pick(ge_i8_plan* p) {
   p->tile = d.tile ? d.tile - 1 : (int)ge::FFN_T256;
   p->splits = 1;
   p->few = few_rows(d);
+  p->cols = few_cols(d);
   if (d.tile || p->few) return;
   const int64_t slots = ceil_div(d.K, 128);
   struct Cost { double fixed, slot, crowd; };
@@ -508,7 +519,7 @@ ge_status_t ge_i8_run(ge_i8_handle_t h, const ge_i8_args_t* a, void* stream) {
   const ge::I8Epilogue ep{a->x_scale, a->w_scale, d.bias ? a->bias : nullptr, d.act, d.dtype == GE_DT_FP32};
   if (h->few) {
     const ge::I8Few f{a->X, a->W, d.residual ? a->residual : nullptr, a->Y, ep, d.ldx, d.ldw, d.ldy, d.ldr,
-                      (int32_t)d.M, (int32_t)d.N, (int32_t)d.K, (int32_t)ge::i8_few_pitch(d.K)};
+                      (int32_t)d.M, (int32_t)d.N, (int32_t)d.K, (int32_t)ge::i8_few_pitch(d.K), h->cols};
     return status_of(ge::launch_i8_few(f, stream_of(stream)));
   }
   const ge::FfnTileInfo ti = ge::ffn_tile_info(h->tile);

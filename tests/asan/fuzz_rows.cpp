@@ -121,6 +121,7 @@ hipError_t launch_i8_few(const I8Few& p, hipStream_t) {
   ++g_launches;
   CHECK(p.M >= 1 && p.M <= kI8FewRows && p.N >= 8 && p.N % 8 == 0 && p.K % 16 == 0);
   CHECK(i8_few_lds(p.M, p.K) <= kI8FewLds && p.x_pitch == i8_few_pitch(p.K) && p.x_pitch % 256 == 32);
+  CHECK(p.cols == kI8FewCols || p.cols == kI8FewCols / 2);
   // whole steps of the tokens' codes lie before the next token's
   CHECK((p.K + kI8FewStep - 1) / kI8FewStep * (int64_t)kI8FewStep <= p.x_pitch);
   CHECK((double)((p.N + kI8FewCols - 1) / kI8FewCols) * 512 < 4294967296.0);

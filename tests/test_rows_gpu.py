@@ -418,6 +418,16 @@ def test_i8_sizes(M, N, K, tile):
     rp.check(Y, *rp.int8(*x, "none", FP32), "Y")
 
 
+@pytest.mark.parametrize("N", [8, 2040, 2048, 2056, 4096, 4104, 6144, 6152])
+@pytest.mark.parametrize("M", [1, 4, 5, 17])
+def test_i8_few_tokens_where_workgroups_change(M, N):
+    x = i8_inputs(M, N, 528, BF16, True, True)
+    Y, plan = run_i8(*x, "none", BF16, pads=(0, 0, 8, 16))
+    assert "few rows" in plan.describe()
+    rp.check(Y, *rp.int8(*x, "none", BF16), "Y")
+    assert torch.equal(Y, run_i8(*x, "none", BF16, rows.GE_I8_TILE_64)[0])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
