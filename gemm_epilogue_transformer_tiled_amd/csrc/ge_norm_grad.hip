@@ -5,7 +5,7 @@
 // row, so it adds up dgain and dbias of its columns in registers over all rows of its workgroup, and
 // a workgroup leaves one partial sum per column; a second launch adds these in 64 bits, in a fixed order.
 // (Atomic adds would need no second launch, but their order changes the last bits.)  Measured: 16384 x 4096 bf16 with
-// dropout 0.1, 671 MB, 113 us, 5.9 TB/s; 1001 x 1021 fp32 10.5 us; 4096 x 16384 bf16 104 us, 5.2 TB/s; 2048 x 32768 133
+// dropout 0.1, 671 MB, 113 us, 5.9 TB/s; 1001 x 1021 fp32 10.1 us; 4096 x 16384 bf16 104 us, 5.2 TB/s; 2048 x 32768 133
 // us (with everything in registers, which spilled, 283 and 801 us).
 #include "ge_rows_common.h"
 
@@ -18,7 +18,7 @@ template <class E, int TR, int V, bool TAIL, bool DROP, int POLICY>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
   __shared__ float red[2][2][NT / 64];
-  __shared__ float gsum[RPW > 1 ? (RPW - 1) * 8 * TR * V : 1];
+  __shared__ f32x4 meet[RPW > 1 ? 4 * RPW * TR * V : 1];
   // WIDE: more than a vector a thread of the largest workgroup, which has 128 registers a thread.  dgain's sums then lie
   // in LDS, each thread's in places of its own, and e and n are taken again from dY and S after the exchange.  AHEAD: the
   // next row's loads have room.  LATE: the gain and dS are loaded where they are used.  TWICE: dY is loaded again for
@@ -195,28 +195,34 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) dgain[i][j] = wide_sum[(2 * i + j / 4) * TR + t][j % 4];
+  if constexpr (RPW > 1) {
+    // the rows taken at once meet in LDS and are added in their order, a vector of columns a thread
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float(&a)[V][8] = which ? dbias : dgain;
-    if constexpr (RPW > 1) {
-      // the rows taken at once meet in LDS and are added in their order
-      if (which) __syncthreads();
-      if (sub > 0)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+      for (int h = 0; h < 2; ++h) {
+        f32x4* const at = meet + 4 * TR * V * sub + 2 * (t + TR * i) + h;
+        at[0] = f32x4{dgain[i][4 * h], dgain[i][4 * h + 1], dgain[i][4 * h + 2], dgain[i][4 * h + 3]};
+        at[2 * TR * V] = f32x4{dbias[i][4 * h], dbias[i][4 * h + 1], dbias[i][4 * h + 2], dbias[i][4 * h + 3]};
+      }
+    __syncthreads();
+    for (int q = threadIdx.x; q < 2 * TR * V; q += NT) {
+      f32x4 a = meet[2 * q], b = meet[2 * q + 1];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) gsum[((sub - 1) * V * 8 + i * 8 + j) * TR + t] = a[i][j];
-      __syncthreads();
-      if (sub == 0)
-        for (int q = 0; q < RPW - 1; ++q)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[i][j] += gsum[(q * V * 8 + i * 8 + j) * TR + t];
+      for (int r = 1; r < RPW; ++r) {
+        a += meet[4 * TR * V * r + 2 * q];
+        b += meet[4 * TR * V * r + 2 * q + 1];
+      }
+      const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const int which = q / (TR * V);
+      put<float, TAIL>(out + which * d, 8 * (q - which * TR * V), d, rounded(v, float()));
     }
-    if (sub == 0)
+  } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) put<float, TAIL>(out + which * d, 8 * (t + TR * i), d, rounded(a[i], float()));
+    for (int i = 0; i < V; ++i) {
+      put<float, TAIL>(out, 8 * (t + TR * i), d, rounded(dgain[i], float()));
+      put<float, TAIL>(out + d, 8 * (t + TR * i), d, rounded(dbias[i], float()));
+    }
   }
 }
 
