@@ -355,25 +355,21 @@ void ffn_product(LAUNCH l) {
             acc[op][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[op][i], f.a[j], acc[op][i][j], 0, 0, 0);
         }
   };
-  // The scales and the bias of the product of codes: loaded here, a trip to memory before they are needed.
-  // (four columns of the epilogue's second phase a lane; N is a multiple of 8: all four or none)
-  float i8_sx[I8 ? T::FM : 1];
-  f32x4_t i8_sw = f32x4_t{}, i8_bias = f32x4_t{};
+  // The scales and the bias of the product of codes: loaded here, a trip to memory before they are needed,
+  // range-checked without a branch and kept as they come, so that nothing waits for them before the operands' loads.
+  // (four columns of the epilogue's second phase a lane; N is a multiple of 8: all four or none; of bf16 the first
+  // eight bytes count)
+  uint32_t i8_sx[I8 ? T::FM : 1];
+  u32x4_t i8_sw = u32x4_t{}, i8_bias = u32x4_t{};
   if constexpr (I8) {
     const I8Epilogue& q = l.ep;
+    const uint32_t size = q.wide ? 4u : 2u, col = (uint32_t)(wn0 + 4 * (lane % (T::WN / 4)));
+    const __amdgpu_buffer_rsrc_t sx_rs = make_rsrc(q.x_scale + m0, 4 * (int64_t)mrows);
 #pragma unroll
-    for (int j = 0; j < T::FM; ++j) {
-      const int ml = wm0 + 16 * j + (int)l16;
-      i8_sx[j] = ml < mrows ? q.x_scale[m0 + ml] : 0.0f;
-    }
-    const int col = wn0 + 4 * (lane % (T::WN / 4)), n = n0 + col;
-    if (col < ncols) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        i8_sw[e] = q.w_scale[n + e];
-        if (q.bias) i8_bias[e] = q.wide ? ((const float*)q.bias)[n + e] : bf16_lo(((const uint16_t*)q.bias)[n + e]);
-      }
-    }
+    for (int j = 0; j < T::FM; ++j) i8_sx[j] = __builtin_amdgcn_raw_buffer_load_b32(sx_rs, 4u * ((uint32_t)(wm0 + 16 * j) + l16), 0, 0);
+    i8_sw = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(q.w_scale + n0, 4 * (int64_t)ncols), 4u * col, 0, 0);
+    i8_bias = __builtin_amdgcn_raw_buffer_load_b128(
+        make_rsrc((const unsigned char*)q.bias + (q.bias ? (int64_t)n0 * size : 0), q.bias ? (int64_t)ncols * size : 0), size * col, 0, 0);
   }
   // a workgroup barrier that no LDS access moves across (the waits are explicit)
   auto barrier = [] {
@@ -520,12 +516,24 @@ void ffn_product(LAUNCH l) {
     };
     // Whole rings (slots past the end read zeros): with an exit after every slot the compiler saw paths
     // on which a slot is read right after its loads were issued, and waited for all loads each ring.
-    for (int s = slot0; s < slot1; s += NS) {
+    // (Codes: whole rings while they last, then single slots.)
+    int s = slot0;
+    for (; I8 ? s + NS <= slot1 : s < slot1; s += NS) {
       turn(GE_I(0), s);
       turn(GE_I(1), s + 1);
       if constexpr (NS > 2) turn(GE_I(2), s + 2);
       if constexpr (NS > 3) turn(GE_I(3), s + 3);
       if constexpr (NS > 4) turn(GE_I(4), s + 4);
+    }
+    if constexpr (I8) {
+      static_assert(NS == 4, "slots of the last ring");
+      if (s < slot1) {
+        turn(GE_I(0), s);
+        if (s + 1 < slot1) {
+          turn(GE_I(1), s + 1);
+          if (s + 2 < slot1) turn(GE_I(2), s + 2);
+        }
+      }
     }
   }
   };
@@ -640,6 +648,10 @@ void ffn_product(LAUNCH l) {
       constexpr int A = decltype(act_c)::value;
       constexpr bool WIDE = decltype(wide_c)::value;
       constexpr uint32_t size = WIDE ? 4u : 2u;
+      float bias[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        bias[e] = WIDE ? __uint_as_float(i8_bias[e]) : (e & 1) ? bf16_hi(i8_bias[e >> 1]) : bf16_lo(i8_bias[e >> 1]);
       // stores of the largest tiles go "nt": their outputs pass what the caches keep (8192 x 4096 x 11008: 323 -> 317 us)
       constexpr int NT = T::PP ? 2 : 0;
       auto rs_of = [&](const void* base, int64_t ld) {
@@ -671,7 +683,7 @@ void ffn_product(LAUNCH l) {
           for (int i = 0; i < T::FN; ++i) {
             f32x4_t t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = (float)acc[0][i][2 * j + par][e] * i8_sx[2 * j + par];
+            for (int e = 0; e < 4; ++e) t[e] = (float)acc[0][i][2 * j + par][e] * __uint_as_float(i8_sx[2 * j + par]);
             *(f32x4_t*)(ep + (16 * par + (int)l16) * T::EP_LD + 16 * i + 4 * (int)q16) = t;
           }
 #pragma unroll
@@ -679,7 +691,7 @@ void ffn_product(LAUNCH l) {
           f32x4_t y = *(const f32x4_t*)(ep + (ps * RPP + p2_row) * T::EP_LD + p2_col);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            y[e] = i8_output<A>(y[e], i8_sw[e], i8_bias[e], p.E1 ? __uint_as_float(rv[ps][e]) : -0.0f);
+            y[e] = i8_output<A>(y[e], __uint_as_float(i8_sw[e]), bias[e], p.E1 ? __uint_as_float(rv[ps][e]) : -0.0f);
           }
           const uint32_t off = at(wm0 + 32 * j + ps * RPP + p2_row, p.ldy);
           if constexpr (WIDE) {
