@@ -387,14 +387,18 @@ bool grid_fits(int tile, int64_t M, int64_t N) {
   return (double)ceil_div(M, ti.bm) * (double)ceil_div(N, ti.bn) * (tile == ge::FFN_T64 ? 256 : 512) <= 4294967295.0;
 }
 
-// Whether the few-row kernel takes the product: the tokens' codes fit a workgroup's LDS, and several workgroups
-// fit a compute unit, unless there are no more of them than units.  (17 tokens at 11008 x 4096, 70 KB: 16.0 us in both;
-// 27 tokens, 111 KB: 21.4 against 16.3 in tiles, but 8.4 against 9.4 at 4096 x 4096, 256 workgroups.)
+// Whether the few-row kernel takes the product (weights from memory, against the tiles, us).  Where each workgroup has a compute
+// unit to itself, the tokens' codes only have to fit its LDS (4096 x 4096, 1 to 32 tokens: 6.0 to 7.8 against 7.9 to 8.0; 2856
+// x 1040, 27 tokens: 4.8 against 5.5).  Where several share one, two have to fit, and the tokens' way to LDS counts: up to 12
+// tokens (11008 x 4096: 14.4 against 15.2; 24 tokens 19.9 against 15.3), 8 where K is long (8192 x 8192: 17.4 against
+// 19.3, 12 tokens 20.2 against 19.6; 5120 x 5120: 10.4 against 10.0, 16 tokens 13.0 against 10.2), and none where they
+// come in rounds of little work each (32000 x 1024: 12.7 against 10.8, x 4096 28 against 35).
 // (Fewer than 2^22 outputs a token, the most that a pitch allows: the launch's threads fit 32 bits.)
 bool few_rows(const ge_i8_desc_t& d) {
   if (d.tile || d.M > ge::kI8FewRows) return false;
-  const int64_t lds = ge::i8_few_lds(d.M, d.K);
-  return lds <= (ceil_div(d.N, ge::kI8FewCols) <= 256 ? ge::kI8FewLds : ge::kI8FewLds / 2);
+  const int64_t lds = ge::i8_few_lds(d.M, d.K), groups = ceil_div(d.N, ge::kI8FewCols);
+  if (groups <= 256) return lds <= ge::kI8FewLds;
+  return d.M <= (d.K <= 4096 ? 12 : 8) && lds <= ge::kI8FewLds / 2 && (groups <= 768 || d.K > 2048);
 }
 
 // Columns of its workgroups: half as many where each workgroup then still has a compute unit to itself (one token: 264 x 11008
