@@ -74,7 +74,7 @@ __device__ __forceinline__ void put16(void* p, u32x4 v) {
 // Values col .. col + 7 of a row of d, zeros past its end.  TAIL: d is no multiple of eight.  The row's last vector is
 // then loaded from its last eight values, and settle() shifts them to their places when they are used: nothing
 // waits for a load when it is made.  (Value by value, and put together at once, the last vector held up its whole row:
-// norm of 16432 x 1021 bf16 30.7 us and its gradient 63.4.)
+// norm of 16432 x 1021 bf16 31 us against 25, its gradient 63 against 44.)
 template <class E, bool TAIL, int POLICY = 0>
 __device__ __forceinline__ Raw<E> fetch(const E* row, int col, int d) {
   Raw<E> r = zero<E>();
