@@ -108,11 +108,13 @@ class _RowsPlan(_Plan):
     """A plan of this library: ``_kind`` is the operator's part of the C names."""
 
     _kind = None
+    _calls = ("forward", "backward")
     workspace = None             # of plans that need one
 
     def _make(self) -> None:
         create = getattr(lib, f"ge_{self._kind}_create")
         self._create(lambda out: create(ctypes.byref(self.desc), out), f"ge_{self._kind}_create")
+        self._fns = {call: getattr(lib, f"ge_{self._kind}_{call}") for call in self._calls}
 
     def _workspace_size(self) -> int:
         n = _sz()
@@ -131,16 +133,14 @@ class _RowsPlan(_Plan):
     def _call(self, call: str, args: Args, stream: Optional[int]) -> None:
         """Checks the pack once for this plan and this call, then makes it."""
         stream = self._stream(stream)
-        fits = args._fits.get(self, ())
-        if call not in fits:
+        if call not in args._fits.get(self, ()):
             getattr(self, "_fit_" + call)(args, stream)
-            args._fits[self] = (*fits, call)
+            args._fits[self] = (*args._fits.get(self, ()), call)
         if self.workspace is not None and args.tensors["workspace"] is None:
             args.c.workspace, args.c.workspace_bytes = self.workspace.data_ptr(), self.workspace.numel()
-        name = f"ge_{self._kind}_{call}"
-        st = getattr(lib, name)(self.handle, args._ref, stream)
+        st = self._fns[call](self.handle, args._ref, stream)
         if st != GE_OK:
-            raise GemmEpilogueError(st, name)
+            raise GemmEpilogueError(st, f"ge_{self._kind}_{call}")
 
     def close(self) -> None:
         if self.handle:
@@ -287,6 +287,7 @@ class RowQuant(_RowsPlan):
     max |x| / 127, code = x / scale to the nearest integer.  ``ld``: leading dimensions that differ (ldx, ldq)."""
 
     _kind = "quant"
+    _calls = ("run",)
 
     def __init__(self, rows: int, d: int, dtype=torch.bfloat16, device="cuda", **ld: int):
         super().__init__(device)
@@ -317,6 +318,7 @@ class Int8Linear(_RowsPlan):
     differ (ldx, ldw, ldy, ldr)."""
 
     _kind = "i8"
+    _calls = ("run",)
 
     def __init__(self, M: int, N: int, K: int, act: str = "none", bias: bool = False, residual: bool = False,
                  dtype=torch.bfloat16, tile: Optional[int] = None, device="cuda", **ld: int):
