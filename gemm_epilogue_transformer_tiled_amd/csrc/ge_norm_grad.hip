@@ -78,7 +78,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
     Row q{};
     if constexpr (AHEAD) {
       q = next;
-      if (row + step < p.rows) load(next, row + step, t); // on its way while this row is computed
+      if (row + step < p.rows) load(next, row + step, t);              // on its way while this row is computed
     } else {
       load(q, row, t);
     }
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
     }
     const float mean = q.mean, rstd = q.rstd;
     float e[V][8], n[V][8], se = 0.0f, sen = 0.0f;
-    auto again = [&](int i, int t) {                          // e and n of vector i
+    auto again = [&](int i, int t) {                   // e and n of vector i
       if constexpr (WIDE && !LATE) landed(gain[i]);    // (kept as it lies in memory)
       Raw<E> of = zero<E>();
       if constexpr (!LATE) of = gain[i];
