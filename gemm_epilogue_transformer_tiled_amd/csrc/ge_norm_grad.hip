@@ -1,7 +1,7 @@
 // Layer norm of rows: the backward pass with the sums of the gain's and the bias' gradients (gfx950).
 //
 // Memory-bound: dY, S (and dS) are read once, dX (and dR) written once.  A row lies in registers as in the
-// forward pass; mean(e) and mean(e n) are taken in one exchange.  A thread holds the same columns of every
+// forward pass; the sums behind mean(e) and mean(e n) are taken in one exchange.  A thread holds the same columns of every
 // row, so it adds up dgain and dbias of its columns in registers over all rows of its workgroup, and
 // a workgroup leaves one partial sum per column; a second launch adds these in 64 bits, in a fixed order.
 // (Atomic adds would need no second launch, but their order changes the last bits.)  Measured: 16384 x 4096 bf16 with
@@ -20,7 +20,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
   __shared__ float red[2][2][NT / 64];
   __shared__ f32x4 meet[RPW > 1 ? 4 * RPW * TR * V : 1];
   // WIDE: more than a vector a thread of the largest workgroup, which has 128 registers a thread.  dgain's sums then lie
-  // in LDS, each thread's in places of its own, and e and n are taken again from dY and S after the exchange.  AHEAD: the
+  // in LDS, each thread's in places of its own, and e and c are taken again from dY and S after the exchange.  AHEAD: the
   // next row's loads have room.  LATE: the gain and dS are loaded where they are used.  TWICE: dY is loaded again for
   // its second use (fp32 rows past 16384; some registers still spill there, 1024 x 32768 178 us, 3.0 TB/s).
   constexpr bool WIDE = TR == 1024 && V > 1;
@@ -89,15 +89,18 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
       if (!LATE && p.ds) settle<TAIL>(q.ds[i], 8 * (t + TR * i), d);
     }
     const float mean = q.mean, rstd = q.rstd;
-    float e[V][8], n[V][8], se = 0.0f, sen = 0.0f;
-    auto again = [&](int i, int t) {                   // e and n of vector i
+    float e[V][8], c[V][8], se = 0.0f, sec = 0.0f;
+    // e and c = s - mean of vector i.  The row's sum is that of e c, not of e n with n = c rstd: past the row's end, where
+    // dy, e and s are 0, n can be too large for a number (rows of nearly equal values far from zero), and 0 times it is
+    // none.  (What dgain gets of it there is not stored.)
+    auto again = [&](int i, int t) {
       if constexpr (WIDE && !LATE) landed(gain[i]);    // (kept as it lies in memory)
       Raw<E> of = zero<E>();
       if constexpr (!LATE) of = gain[i];
       else if (p.gain) of = fetch_settled<E, TAIL>((const E*)p.gain, 8 * (t + TR * i), d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[i][j] = (get(q.s[i], j) - mean) * rstd;
+        c[i][j] = get(q.s[i], j) - mean;
         e[i][j] = p.gain ? get(q.dy[i], j) * get(of, j) : get(q.dy[i], j);
       }
     };
@@ -109,11 +112,10 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
         for (int j = 0; j < 8; ++j) dgain[i][j] = wide_sum[(2 * i + j / 4) * TR + t][j % 4];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // (past the row's end dy is 0: whatever n is there, it adds nothing)
         const float dy = get(q.dy[i], j);
         se += e[i][j];
-        sen = fmaf(e[i][j], n[i][j], sen);
-        dgain[i][j] = fmaf(dy, n[i][j], dgain[i][j]);
+        sec = fmaf(e[i][j], c[i][j], sec);
+        dgain[i][j] = fmaf(dy, c[i][j] * rstd, dgain[i][j]);
         dbias[i][j] += dy;
       }
       if constexpr (WIDE)
@@ -121,29 +123,29 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
         for (int h = 0; h < 2; ++h)
           wide_sum[(2 * i + h) * TR + t] = f32x4{dgain[i][4 * h], dgain[i][4 * h + 1], dgain[i][4 * h + 2], dgain[i][4 * h + 3]};
       if constexpr (WIDE) {                            // one vector after the other: less is held
-        asm volatile("" : "+v"(se), "+v"(sen));
+        asm volatile("" : "+v"(se), "+v"(sec));
 #pragma unroll
         for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(dbias[i][j]));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     se = wave_sum(se);
-    sen = wave_sum(sen);
+    sec = wave_sum(sec);
     if constexpr (TR > 64) {
       const int w = (int)threadIdx.x >> 6;
       if ((threadIdx.x & 63) == 0) {
         red[turn][0][w] = se;
-        red[turn][1][w] = sen;
+        red[turn][1][w] = sec;
       }
       __syncthreads();
-      se = sen = 0.0f;
+      se = sec = 0.0f;
 #pragma unroll
       for (int k = 0; k < TR / 64; ++k) {
         se += red[turn][0][k];
-        sen += red[turn][1][k];
+        sec += red[turn][1][k];
       }
     }
-    const float me = se / of_d, men = sen / of_d;
+    const float me = se / of_d, mec = sec / of_d * rstd * rstd;
     // The next row has landed before this one's stores go out: a wait for loads behind stores would wait for
     // the stores too.
     if constexpr (AHEAD) {
@@ -158,7 +160,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
     const int u = place();
     if constexpr (WIDE)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {                    // (not the e and n of before: they would be kept)
+      for (int i = 0; i < V; ++i) {                    // (not the e and c of before: they would be kept)
         if constexpr (!TWICE) landed(q.dy[i]);
         landed(q.s[i]);
       }
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
       float g[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        g[j] = rstd * fmaf(-n[i][j], men, e[i][j] - me);
+        g[j] = rstd * fmaf(-c[i][j], mec, e[i][j] - me);
         if (p.ds) g[j] += get(ds, j);
       }
       if (p.dr) put<E, TAIL, POLICY>((E*)p.dr + row * p.lddr, col, d, rounded(g, E()));
