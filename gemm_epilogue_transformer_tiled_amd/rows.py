@@ -163,6 +163,13 @@ def _pitches(d: int, names, ld) -> dict:
     return {name: ld.get(name, d) for name in names}
 
 
+def _site(site: int) -> int:
+    """The dropout's number in its step (ctypes would keep its low 32 bits: another site's masks)."""
+    if not 0 <= site < 1 << 32:
+        raise ValueError(f"site {site}: 0 to 2**32 - 1")
+    return site
+
+
 def make_norm_args(X=None, residual=None, S=None, Y=None, gain=None, bias=None, mean=None, rstd=None, rng=None, dY=None, dS=None,
                    dX=None, dR=None, dgain=None, dbias=None, workspace=None) -> Args:
     """Pointer pack of the layer norm: matrices [rows][d], gain, bias [d] of the plan's type (None: ones,
@@ -178,7 +185,7 @@ class LayerNorm(_RowsPlan):
     writes Y and, where they are given, S, mean and rstd.  ``backward`` reads dY, S (X itself where there is
     neither residual nor dropout), mean, rstd, gain, dS where it is given (the gradient that reaches S
     from elsewhere) and rng; writes dX, dR (the residual's gradient), dgain and dbias, each if given.
-    ``site`` tells the dropouts of one step apart.  ``ld``: leading dimensions that differ (ldx, ldr, lds,
+    ``site`` (32 bits) tells the dropouts of one step apart.  ``ld``: leading dimensions that differ (ldx, ldr, lds,
     ldy, lddy, ldds, lddx, lddr)."""
 
     _kind = "norm"
@@ -186,8 +193,8 @@ class LayerNorm(_RowsPlan):
     def __init__(self, rows: int, d: int, eps: float = 1e-5, dtype=torch.bfloat16, residual: bool = False,
                  dropout: float = 0.0, site: int = 0, device="cuda", **ld: int):
         super().__init__(device)
-        self.desc = ge_norm_desc_t(rows=rows, d=d, dtype=self._dtype(dtype), residual=int(residual), site=site, dropout=dropout,
-                                   eps=eps, **_pitches(d, ("ldx", "ldr", "lds", "ldy", "lddy", "ldds", "lddx", "lddr"), ld))
+        self.desc = ge_norm_desc_t(rows=rows, d=d, dtype=self._dtype(dtype), residual=int(residual), site=_site(site),
+                                   dropout=dropout, eps=eps, **_pitches(d, ("ldx", "ldr", "lds", "ldy", "lddy", "ldds", "lddx", "lddr"), ld))
         self._make()
         self.drops = self.desc.dropout * 65536 >= 0.5
         # (the workspace is made by the first backward that needs it)
@@ -249,7 +256,7 @@ class Dropout(_RowsPlan):
     def __init__(self, rows: int, d: int, p: float, dtype=torch.bfloat16, residual: bool = False, site: int = 0, device="cuda",
                  **ld: int):
         super().__init__(device)
-        self.desc = ge_dropout_desc_t(rows=rows, d=d, dtype=self._dtype(dtype), residual=int(residual), site=site, p=p,
+        self.desc = ge_dropout_desc_t(rows=rows, d=d, dtype=self._dtype(dtype), residual=int(residual), site=_site(site), p=p,
                                       **_pitches(d, ("ldx", "ldr", "ldy", "lddy", "lddx"), ld))
         self._make()
 
