@@ -24,6 +24,10 @@
  * each other, except where an operator says that an output may be an input itself (same pointer and
  * leading dimension).
  *
+ * Sizes: besides what each operator says, the row operators (ge_norm, ge_dropout, ge_quant) take up to 2^40 rows,
+ * leading dimensions up to 2^40, and rows times each leading dimension up to 10^18; what is larger is
+ * GE_ERR_UNSUPPORTED.
+ *
  * Errors: every call returns a status, nothing is enqueued unless it is GE_OK (GE_ERR_HIP: a
  * launch failed, and earlier launches of the same call may have run), nothing aborts.
  */
@@ -69,9 +73,13 @@ extern "C" {
  * elsewhere (the residual stream goes on past the norm).
  *
  * Element types: X, R, S, Y, gain, bias and their gradients all bf16 or all fp32; mean, rstd, dgain
- * and dbias fp32.  rows >= 0 (any), 1 <= d <= 32768.  Pointers need their element's alignment only;
+ * and dbias fp32.  rows >= 0, 1 <= d <= 32768.  Pointers need their element's alignment only;
  * 16-byte aligned rows are fastest.  Forward: S and Y may be X or R; backward: dX and dR may be dY, S or
  * dS.  Sums over rows are taken in a fixed order: equal calls give equal bits.
+ *
+ * Range: the arithmetic is fp32's.  A row whose sum of values, or of squared deviations (each about 1.8e19 or more),
+ * passes 3.4e38 does not get the formula's outputs, nor does a row of equal values with eps = 0 (NaN).  Such rows, and
+ * rows with infinities or NaN, change no other row's outputs; dgain and dbias are sums over all of them.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
   int64_t rows, d;
@@ -119,8 +127,8 @@ void ge_norm_destroy(ge_norm_handle_t handle);
 
 /* ---------------------------------------------------------------------------------------------
  * Dropout of rows of d values:  forward Y = drop(X) (+ R),  backward dX = drop(dY)  with the same mask
- * (fp32 arithmetic, one rounding).  All of one type, bf16 or fp32.  rows, d >= 0 (any).  Y may be X or
- * R, dX may be dY.
+ * (fp32 arithmetic, one rounding).  All of one type, bf16 or fp32.  rows >= 0, 0 <= d <= 2^31 - 16 (and
+ * rows * ceil(d / 8) <= 2^32, as above).  Y may be X or R, dX may be dY.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
   int64_t rows, d;
@@ -156,7 +164,7 @@ void ge_dropout_destroy(ge_dropout_handle_t handle);
  *
  * The exact quotient decides, ties go to the even code.  A row of zeros (or of no values) has scale 0
  * and codes 0.  A row that holds a NaN or an infinity has scale NaN and codes 0: a product with it is NaN.
- * X bf16 or fp32 [rows][ldx], codes [rows][ldq], scale [rows].  rows >= 0 (any), 0 <= d <= 32768.
+ * X bf16 or fp32 [rows][ldx], codes [rows][ldq], scale [rows].  rows >= 0, 0 <= d <= 32768.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
   int64_t rows, d;
@@ -184,12 +192,14 @@ void ge_quant_destroy(ge_quant_handle_t handle);
  *   Y[m][n] = act(x_scale[m] * w_scale[n] * sum over k of X[m][k] W[n][k] + bias[n]) + R[m][n]
  *
  * The sums are int32 and exact; everything after them is fp32, one rounding at the end.  Y, bias and R
- * all bf16 or all fp32; scales fp32 [M] and [N] (any values: a NaN scale gives NaN).  Activations as in
- * gemm_epilogue.h; a NaN stays NaN with each of them.  Equal calls give equal bits.
+ * all bf16 or all fp32; scales fp32 [M] and [N].  A sum is multiplied with its row's scale first: scales may be any numbers
+ * as long as that product, of a sum up to 2^14 K, stays below 3.4e38 (magnitudes of x_scale up to 1e29 always do); a NaN
+ * scale gives NaN.  Activations as in gemm_epilogue.h; a NaN stays NaN with each of them.  Equal calls give equal bits.
  *
- * Supported: M >= 0 (any value), N >= 0 and a multiple of 8, K >= 0 and a multiple of 16 below 2^17 (sums
+ * Supported: M >= 0, N >= 0 and a multiple of 8, K >= 0 and a multiple of 16 below 2^17 (sums
  * of any codes, -128 among them, fit 32 bits); ldx and ldw multiples of 16, ldy and ldr of 8, all
- * below 2^22 (fp32: ldy and ldr below 2^21); M and N below 2^31 - 512; 16-byte aligned pointers (scales:
+ * below 2^22 (fp32: ldy and ldr below 2^21); M and N below 2^31 - 512, and ceil(M / 256) * ceil(N / 256) below 2^23
+ * (with a tile named, its own rows and columns instead of 256: below 2^23, of 64 below 2^24); 16-byte aligned pointers (scales:
  * 4-byte).  Y may be R.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
