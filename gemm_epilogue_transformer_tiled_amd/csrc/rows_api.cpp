@@ -387,12 +387,15 @@ bool grid_fits(int tile, int64_t M, int64_t N) {
   return (double)ceil_div(M, ti.bm) * (double)ceil_div(N, ti.bn) * (tile == ge::FFN_T64 ? 256 : 512) <= 4294967295.0;
 }
 
-// Whether the few-row kernel takes the product (weights from memory, against the tiles, us).  Where each workgroup has a compute
-// unit to itself, the tokens' codes only have to fit its LDS (4096 x 4096, 1 to 32 tokens: 6.0 to 7.8 against 7.9 to 8.0; 2856
-// x 1040, 27 tokens: 4.8 against 5.5).  Where several share one, two have to fit, and the tokens' way to LDS counts: up to 12
-// tokens (11008 x 4096: 14.4 against 15.2; 24 tokens 19.9 against 15.3), 8 where K is long (8192 x 8192: 17.4 against
-// 19.3, 12 tokens 20.2 against 19.6; 5120 x 5120: 10.4 against 10.0, 16 tokens 13.0 against 10.2), and none where they
-// come in rounds of little work each (32000 x 1024: 12.7 against 10.8, x 4096 28 against 35).
+// Whether the few-row kernel takes the product (N x K, everything from memory, against the tiles, us).  Where each workgroup
+// has a compute unit to itself, the tokens' codes only have to fit its LDS (4096 x 4096: one token 6.5 against 8.2, 16 tokens
+// 8.4 against 8.2, 32 tokens 9.6 against 9.4; 2856 x 1040, 27 tokens 4.6 against 5.0).  Where several share one, two have to
+// fit (11008 x 4096, 27 tokens in 111 KB: 21.9 against 14.2), and the tokens' way to LDS counts: up to 12 tokens (one token:
+// 6144 x 4096 7.5 against 10.2, 11008 x 4096 12.2 against 13.3; 12 tokens: 6144 x 2048 6.7 against 7.8, 8192 x 5120
+// 11.7 against 12.5), 8 where K is long (8192 x 8192 16.6 against 19.1), and none where they come in rounds of little
+// work each (one token: 32000 x 1024 12.5 against 10.0, but x 2064 15.0 against 18.3, x 4096 27 against 33).  The borders are
+// not exact: past 4 tokens K = 4096 would be faster in tiles (8 tokens: 11008 x 4096 14.5 against 13.5), and with all weights
+// in the caches tiles are faster at many sizes from 11008 columns on (one token: 11008 x 4096 9.9 against 9.4).
 // (Fewer than 2^22 outputs a token, the most that a pitch allows: the launch's threads fit 32 bits.)
 bool few_rows(const ge_i8_desc_t& d) {
   if (d.tile || d.M > ge::kI8FewRows) return false;
