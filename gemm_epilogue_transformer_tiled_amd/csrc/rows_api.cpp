@@ -390,7 +390,7 @@ bool grid_fits(int tile, int64_t M, int64_t N) {
 // Whether the few-row kernel takes the product (N x K, everything from memory, against the tiles, us).  Where each workgroup
 // has a compute unit to itself, the tokens' codes only have to fit its LDS (4096 x 4096: one token 6.5 against 8.2, 16 tokens
 // 8.4 against 8.2, 32 tokens 9.6 against 9.4; 2856 x 1040, 27 tokens 4.6 against 5.0).  Where several share one, two have to
-// fit (11008 x 4096, 27 tokens in 111 KB: 21.9 against 14.2), and the tokens' way to LDS counts: up to 12 tokens (one token:
+// fit (11008 x 4096, 27 tokens in 109 KiB: 21.9 against 14.2), and the tokens' way to LDS counts: up to 12 tokens (one token:
 // 6144 x 4096 7.5 against 10.2, 11008 x 4096 12.2 against 13.3; 12 tokens: 6144 x 2048 6.7 against 7.8, 8192 x 5120
 // 11.7 against 12.5), 8 where K is long (8192 x 8192 16.6 against 19.1), and none where they come in rounds of little
 // work each (one token: 32000 x 1024 12.5 against 10.0, but x 2064 15.0 against 18.3, x 4096 27 against 33).  The borders are

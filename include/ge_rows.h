@@ -78,7 +78,8 @@ extern "C" {
  * dS.  Sums over rows are taken in a fixed order: equal calls give equal bits.
  *
  * Range: the arithmetic is fp32's.  A row whose sum of values, or of squared deviations (each about 1.8e19 or more),
- * passes 3.4e38 does not get the formula's outputs, nor does a row of equal values with eps = 0 (NaN).  Such rows, and
+ * passes 3.4e38 does not get the formula's outputs, nor does one whose squared deviations are below 1e-38 (each about
+ * 1e-19 or less) with an eps that is no larger, nor a row of equal values with eps = 0 (NaN).  Such rows, and
  * rows with infinities or NaN, change no other row's outputs; dgain and dbias are sums over all of them.
  * ------------------------------------------------------------------------------------------- */
 typedef struct {
